@@ -1,0 +1,117 @@
+/*
+ * Sequence operators for AMD Instinct MI355X (gfx950): C ABI.
+ *
+ * Two operators over token sequences, each for prompts, single tokens and
+ * training:
+ *
+ *  - window attention. Sequence b has kv_lens[b] keys and values and
+ *    q_lens[b] queries, its last ones: query i stands at position
+ *    p = kv_lens[b] - q_lens[b] + i. It sees the keys j with
+ *        p - window < j <= p,   and   j < sinks with j <= p,
+ *    and with s_j = scale * q_i . k_j over these,
+ *        out_i = sum_j exp(s_j - lse_i) v_j,   lse_i = log sum_j exp(s_j).
+ *    A query that sees nothing (p < 0) has out 0 and lse -infinity. Query
+ *    head h reads key head h / (Hq / Hkv).
+ *  - linear attention with a decay for each head, a = exp(log_decay[h]):
+ *        S_t = a S_(t-1) + k_t v_t^T,   out_t = scale q_t S_t.
+ *
+ * Conventions, beyond those of im2win.h (streams, errors, device memory):
+ *  - Elements are binary16 (dtype 0) or bfloat16 (dtype 1), passed as bit
+ *    patterns. Dot products, softmax statistics and states are fp32.
+ *  - Strides are in elements. The innermost stride of every tensor is 1; the
+ *    other strides of 16-bit tensors are multiples of 8 and their bases
+ *    16-byte aligned. Head sizes are multiples of 8, at most 128.
+ *  - Lengths live on the device and are not read by the host. A length below
+ *    zero counts as zero and one above the tensor's extent as the extent.
+ *  - What lies past a sequence's end is not read (NaN there does no harm) and
+ *    is written as zeros (lse: -infinity). Inside a sequence, a value that is
+ *    not finite may reach the rows of neighbouring queries that its key is
+ *    hidden from, as 0 * infinity does in a product with a masked matrix.
+ *  - Results are the same bits on every call (no atomics, fixed order).
+ *  - No entry point throws or aborts.
+ */
+#ifndef IM2WIN_SEQ_H
+#define IM2WIN_SEQ_H
+
+#include <stddef.h>
+#include <stdint.h>
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* One 16-bit tensor (B, L, H, D): element (b, l, h, d) is at
+ * b*stride_b + l*stride_l + h*stride_h + d. */
+typedef struct {
+    void *p;
+    int64_t stride_b, stride_l, stride_h;
+} seq_tensor;
+
+typedef struct {
+    seq_tensor q;            /* (B, Lq, Hq, D) */
+    seq_tensor k, v;         /* (B, Lk, Hkv, D), or the pool of pages (pages, page, Hkv, D):
+                                stride_b then steps from page to page */
+    seq_tensor out;          /* (B, Lq, Hq, D) */
+    float *lse;              /* (B, Hq, Lq), or NULL (forward only) */
+    const int32_t *q_lens;   /* (B), or NULL: Lq each */
+    const int32_t *kv_lens;  /* (B), or NULL: Lk each */
+    const int32_t *page_table; /* (B, ceil(Lk / page)), or NULL: k, v are whole sequences.
+                                A page number outside the pool makes the outputs that see
+                                it NaN; nothing outside the pool is read. */
+    int64_t table_stride;    /* elements from one sequence's pages to the next */
+    int32_t dtype, B, Lq, Lk, Hq, Hkv, D;
+    int32_t page, pages;     /* tokens of a page and pages of the pool (0 without a table) */
+    int32_t window, sinks;   /* window >= 1, sinks >= 0 */
+    float scale;
+    /* Backward only (zero otherwise). */
+    seq_tensor dout, dq, dk, dv; /* dout, dq as q; dk, dv as k and v */
+} seq_attention;
+
+/*
+ * im2win_seq_attention: out, and lse unless NULL. ws: at least
+ *     im2win_seq_attention_workspace_bytes(a) bytes, 16-byte aligned (0 bytes:
+ *     may be NULL). The bytes depend on the sizes alone. A workspace too
+ *     small: IM2WIN_EWORKSPACE.
+ * im2win_seq_attention_backward: dq, dk, dv from dout and the forward call's
+ *     out and lse. No page table. Workspace as above, from
+ *     im2win_seq_attention_backward_workspace_bytes.
+ * The queries return 0 for arguments that the calls refuse.
+ */
+size_t im2win_seq_attention_workspace_bytes(const seq_attention *a);
+int im2win_seq_attention(const seq_attention *a, void *ws, size_t ws_bytes, void *stream);
+size_t im2win_seq_attention_backward_workspace_bytes(const seq_attention *a);
+int im2win_seq_attention_backward(const seq_attention *a, void *ws, size_t ws_bytes, void *stream);
+
+typedef struct {
+    seq_tensor q, k, v, out;  /* (B, L, H, Dk), (B, L, H, Dk), (B, L, H, Dv), (B, L, H, Dv) */
+    const float *log_decay;   /* (H), each <= 0 (-infinity: nothing is kept) */
+    const float *state_in;    /* (B, H, Dk, Dv) contiguous, or NULL: zeros */
+    float *state_out;         /* the same, or NULL; may be state_in */
+    const int32_t *lens;      /* (B), or NULL: L each */
+    int32_t dtype, B, L, H, Dk, Dv;
+    float scale;
+    /* Backward only (zero otherwise). */
+    seq_tensor dout, dq, dk, dv; /* as out, q, k, v */
+    const float *dstate_out;  /* gradient of state_out, or NULL: zeros */
+    float *dstate_in;         /* gradient of state_in, or NULL */
+} seq_linear;
+
+/*
+ * im2win_seq_linear: out, and the state after each sequence's last token
+ *     unless state_out is NULL. Workspace as above.
+ * im2win_seq_linear_step: one token for each sequence (L = 1, lens NULL);
+ *     state_in is state_out, updated in place. No workspace.
+ * im2win_seq_linear_backward: dq, dk, dv and dstate_in (unless NULL) from
+ *     dout and dstate_out. log_decay is a constant and gets no gradient.
+ */
+size_t im2win_seq_linear_workspace_bytes(const seq_linear *a);
+int im2win_seq_linear(const seq_linear *a, void *ws, size_t ws_bytes, void *stream);
+int im2win_seq_linear_step(const seq_linear *a, void *stream);
+size_t im2win_seq_linear_backward_workspace_bytes(const seq_linear *a);
+int im2win_seq_linear_backward(const seq_linear *a, void *ws, size_t ws_bytes, void *stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* IM2WIN_SEQ_H */

@@ -11,6 +11,12 @@ in the library's HIP kernels.
     ws = pack(x, Hf, Wf, stride)             # the im2win transform itself
     with knobs(f16_rows=-1): ...             # planner overrides (tests, ablation)
 
+Operators over token sequences (sequence.py; C ABI in include/im2win_seq.h):
+
+    out = window_attention(q, k, v, window=1024, sinks=4)      # prompts, single tokens, pages
+    out, state = linear_attention(q, k, v, log_decay)          # and linear_attention_step
+    window_attention_backward, linear_attention_backward       # their gradients
+
 A stride is one int (both axes) or a pair (sh, sw): row stride, then column
 stride. Equal strides go through the single-stride entry points of the C ABI,
 unequal ones through their *_strided twins.
@@ -21,12 +27,18 @@ import ctypes
 
 from . import _lib
 from ._lib import Im2winError, status_string  # noqa: F401
+from .sequence import (linear_attention, linear_attention_backward, linear_attention_step,  # noqa: F401
+                       linear_attention_workspace_bytes, window_attention, window_attention_backward,
+                       window_attention_workspace_bytes)
 
 __all__ = ["conv2d", "conv2d_fused", "pack", "workspace_bytes", "fused_workspace_bytes",
            "output_dims", "strides", "knob_names", "set_knob", "get_knob", "knobs",
            "conv_kernel_name",
            "im2col", "im2col_workspace_bytes", "conv2d_im2col", "conv2d_direct",
            "pack_nhwc", "conv2d_nhwc", "nhwc_workspace_bytes",
+           "window_attention", "window_attention_backward", "window_attention_workspace_bytes",
+           "linear_attention", "linear_attention_step", "linear_attention_backward",
+           "linear_attention_workspace_bytes",
            "Im2winError", "status_string", "load_library"]
 
 

@@ -56,6 +56,20 @@ EXPORTS = {
     "im2win_peak_probe_flops": ([_i, _i, _i], ctypes.c_double),
 }
 
+# The sequence operators (include/im2win_seq.h). Their argument structs are
+# passed as packed bytes.
+SEQ_EXPORTS = {
+    "im2win_seq_attention_workspace_bytes": ([_p], _sz),
+    "im2win_seq_attention": ([_p, _p, _sz, _p], _i),
+    "im2win_seq_attention_backward_workspace_bytes": ([_p], _sz),
+    "im2win_seq_attention_backward": ([_p, _p, _sz, _p], _i),
+    "im2win_seq_linear_workspace_bytes": ([_p], _sz),
+    "im2win_seq_linear": ([_p, _p, _sz, _p], _i),
+    "im2win_seq_linear_step": ([_p, _p], _i),
+    "im2win_seq_linear_backward_workspace_bytes": ([_p], _sz),
+    "im2win_seq_linear_backward": ([_p, _p, _sz, _p], _i),
+}
+
 _lib = None
 
 
@@ -83,7 +97,7 @@ def load() -> ctypes.CDLL:
     # and device pointers and streams would not be valid across the two.
     import torch  # noqa: F401
     L = ctypes.CDLL(LIB_PATH)
-    for name, (args, res) in EXPORTS.items():
+    for name, (args, res) in {**EXPORTS, **SEQ_EXPORTS}.items():
         f = getattr(L, name)
         f.argtypes = args
         f.restype = res

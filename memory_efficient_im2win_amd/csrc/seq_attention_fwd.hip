@@ -1,0 +1,244 @@
+// Window attention, forward: one pass over the visible keys with the running
+// maximum and sum of the softmax.
+//
+// A wave owns 32 flattened rows. For a tile of 64 keys it forms
+// S^T = K Q^T (keys x rows) on the matrix cores, so that a lane holds 32
+// scores of one row: maximum, exponential and sum need no other lane until
+// the end. The probabilities, rounded to the element type (half a step
+// each, independent from key to key; their sum is taken before), are as they lie the
+// right operand of O^T += V^T P^T, with V read transposed from LDS.
+//
+// The running maximum is a reference that only moves when a score passes it
+// by more than 8 in log2 units: the softmax is the same for every reference,
+// terms stay below 2^8, and the accumulators are rarely scaled. In fp16 the
+// terms carry a factor 2^6 more (below 2^14 still), which keeps small ones
+// out of the type's subnormal range.
+//
+// Key tiles go to LDS by direct loads, the next tile's under this tile's
+// products (two buffers, one barrier a tile).
+#include <type_traits>
+
+#include "seq_attention.hpp"
+
+namespace im2win {
+namespace seq {
+namespace {
+
+template <bool BF, int DP, int NW>
+__global__ __launch_bounds__(NW * 64, NW > 2 ? 2 : 1) void attn_fwd_kernel(const AttnParams a)
+{
+    constexpr int LP = row_pitch(DP), KS = DP / 16, MT = DP / 32, TILE = kKeyTile * LP * 2;
+    __shared__ __align__(1024) unsigned char smem[4 * TILE];
+    const u32 lds = (u32)(uintptr_t)(lds_byte*)smem;
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), h = lane >> 5;
+
+    const int id = (int)xcd_tile(blockIdx.x, gridDim.x, a.tiles > 1);
+    const int split = id % a.nsplit, tile = id / a.nsplit % a.tiles, bh = id / a.nsplit / a.tiles;
+    const int b = bh / a.Hkv, hk = bh % a.Hkv;
+    const Span s(a, b);
+
+    const int r0 = tile * (NW * 32), rw = r0 + wave * 32, r = rw + (lane & 31);
+    const int r_end = s.nq * a.G;  // rows past it are empty
+    const int i0 = a.by_group.div(r0), i1 = min((int)a.by_group.div(min(r0 + NW * 32, a.rows) - 1), s.nq - 1);
+    const KeyTiles kt(a, s, i0, i1);
+    const int per = (kt.n + a.nsplit - 1) / a.nsplit;
+    const int it0 = split * per, it1 = min(kt.n, it0 + per);
+
+    // The positions of this wave's rows, and of this lane's.
+    const int pw_lo = s.off + (int)a.by_group.div(rw), pw_hi = s.off + min((int)a.by_group.div(rw + 31), s.nq - 1);
+    const int p = s.off + (int)a.by_group.div(r);
+
+    if (it0 < it1) stage_keys<LP, NW>(a, a.k, a.v, b, hk, kt, kt.at(it0), lds, lds + TILE);
+
+    // A negative scale flips the rows' sign (exact), so that the largest
+    // product is the largest score; a zero one clears them.
+    const float c = fabsf(a.scale) > 0 ? fabsf(a.scale) * kLog2e : 1.0f;
+    const u32 flip = a.scale < 0 ? 0x80008000u : 0u, keep = a.scale == 0 ? 0u : 0xffffffffu;
+    u32x4_t q[KS];
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+        q[ks] = *(const u32x4_t*)row_ptr(a, a.q, b, hk, r, r_end, ks * 16 + h * 8);
+        q[ks] = (q[ks] & keep) ^ flip;
+    }
+
+    floatx16_t o[MT] = {};
+    constexpr float kLift = BF ? 0.0f : 6.0f;
+    float m = -INFINITY, mc = 0, l = 0;  // reference, the same in log2 units, this lane's sum
+    for (int it = it0; it < it1; ++it) {
+        const u32 buf = lds + ((it - it0) & 1) * (2 * TILE), nbuf = lds + ((it - it0 + 1) & 1) * (2 * TILE);
+        sync_all();
+        if (it + 1 < it1) stage_keys<LP, NW>(a, a.k, a.v, b, hk, kt, kt.at(it + 1), nbuf, nbuf + TILE);
+        const int k0 = kt.at(it) * kKeyTile;
+        if (rw >= r_end || k0 > pw_hi || (k0 + kKeyTile - 1 <= pw_lo - a.window && k0 >= a.sinks)) continue;
+
+        floatx16_t sc[2] = {};
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+                sc[kb] = mfma<BF>(read_rows<LP>(buf, kb * 32 + (lane & 31), ks * 16 + h * 8), q[ks], sc[kb]);
+        if (k0 + kKeyTile - 1 > pw_lo || k0 <= pw_hi - a.window) {
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int j = k0 + kb * 32 + 8 * (i / 4) + 4 * h + i % 4;
+                    const bool seen = j <= p && (j > p - a.window || j < a.sinks);
+                    sc[kb][i] = seen ? sc[kb][i] : -INFINITY;
+                }
+        }
+        float top = sc[0][0];
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = fmaxf(top, sc[kb][i]);
+        // Moves the reference (the two lanes of a row alike).
+        if (__ballot(m == -INFINITY ? top > m : top * c > mc + 8.0f)) {
+            const float m1 = fmaxf(m, half_max(top));
+            const float mc1 = m1 == -INFINITY ? 0.0f : m1 * c;
+            const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mc - mc1);
+            m = m1;
+            mc = mc1;
+            l *= f;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) o[mt] *= f;
+        }
+        u32x4_t pr[4];
+        const float base = kLift - mc;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+                const float e0 = __builtin_amdgcn_exp2f(fmaf(sc[kb][i], c, base));
+                const float e1 = __builtin_amdgcn_exp2f(fmaf(sc[kb][i + 1], c, base));
+                l += e0;
+                l += e1;
+                pr[kb * 2 + i / 8][i % 8 / 2] = pack2<BF>(e0, e1);
+            }
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+                o[mt] = mfma<BF>(read_cols<LP>(buf + TILE, ks * 16, mt * 32), pr[ks], o[mt]);
+    }
+
+    if (r >= a.rows) return;
+    l = half_sum(l);
+    const int i = a.by_group.div(r), g = r - i * a.G;
+    const bool there = r < r_end;
+    if (a.nsplit > 1) {
+        const int64_t at = ((int64_t)split * a.B * a.Hkv + bh) * a.rows + r;
+        float* part = a.part + at * (a.D + 2);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+                const int d = mt * 32 + 8 * (j / 4) + 4 * h + j % 4;
+                floatx2_t w = {o[mt][j], o[mt][j + 1]};
+                if (d < a.D) *(floatx2_t*)(part + 2 + d) = w;
+            }
+        if (h == 0) {
+            floatx2_t w = {m == -INFINITY ? -INFINITY : mc - kLift, l};
+            *(floatx2_t*)part = w;
+        }
+        return;
+    }
+    const float inv = there && l != 0 ? 1.0f / l : 0.0f;
+    unsigned char* out = a.out.p + b * a.out.sb + i * a.out.sl + (int64_t)(hk * a.G + g) * a.out.sh;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+            const int d = mt * 32 + 8 * (j / 4) + 4 * h;
+            u32x2_t w = {pack2<BF>(o[mt][j] * inv, o[mt][j + 1] * inv),
+                         pack2<BF>(o[mt][j + 2] * inv, o[mt][j + 3] * inv)};
+            if (!there) w = (u32x2_t)(0u);
+            if (d < a.D) *(u32x2_t*)(out + d * 2) = w;
+        }
+    if (a.lse && h == 0)
+        a.lse[((int64_t)b * a.Hq + hk * a.G + g) * a.Lq + i] =
+            there && l != 0 ? (mc - kLift + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+}
+
+// Joins the splits of a row: out = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s.
+// D / 4 lanes hold a row, 4 dimensions each.
+template <bool BF>
+__global__ __launch_bounds__(256) void attn_join_kernel(const AttnParams a, int lanes)
+{
+    const int per = 256 / lanes, sub = threadIdx.x / lanes, d = threadIdx.x % lanes * 4;
+    const int64_t row = (int64_t)blockIdx.x * per + sub, all = (int64_t)a.B * a.Hkv * a.rows;
+    if (sub >= per || row >= all || d >= a.D) return;
+    const int bh = (int)(row / a.rows), r = (int)(row % a.rows), b = bh / a.Hkv, hk = bh % a.Hkv;
+    const int i = a.by_group.div(r), g = r - i * a.G;
+    const Span s(a, b);
+    const float* part = a.part + row * (a.D + 2);
+    const int64_t step = all * (a.D + 2);
+    float m = -INFINITY, l = 0;
+    floatx4_t o = {0, 0, 0, 0};
+    if (i < s.nq) {
+        for (int j = 0; j < a.nsplit; ++j) m = fmaxf(m, part[j * step]);
+        const float mu = m == -INFINITY ? 0.0f : m;
+        for (int j = 0; j < a.nsplit; ++j) {
+            const float* x = part + j * step;
+            const floatx2_t lo = *(const floatx2_t*)(x + 2 + d), hi = *(const floatx2_t*)(x + 4 + d);
+            const float f = __builtin_amdgcn_exp2f(x[0] - mu);
+            l += f * x[1];
+            o[0] += f * lo[0], o[1] += f * lo[1], o[2] += f * hi[0], o[3] += f * hi[1];
+        }
+    }
+    const float inv = l != 0 ? 1.0f / l : 0.0f;
+    unsigned char* out = a.out.p + b * a.out.sb + i * a.out.sl + (int64_t)(hk * a.G + g) * a.out.sh;
+    u32x2_t w = {pack2<BF>(o[0] * inv, o[1] * inv), pack2<BF>(o[2] * inv, o[3] * inv)};
+    *(u32x2_t*)(out + d * 2) = w;
+    if (a.lse && d == 0)
+        a.lse[((int64_t)b * a.Hq + hk * a.G + g) * a.Lq + i] =
+            l != 0 ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+}
+
+template <bool BF, int NW>
+int run(const AttnParams& a, hipStream_t st)
+{
+    const unsigned grid = (unsigned)((int64_t)a.B * a.Hkv * a.tiles * a.nsplit);
+    return with_head(a.D, [&](auto DP) {
+        attn_fwd_kernel<BF, DP.value, NW><<<grid, NW * 64, 0, st>>>(a);
+        return launch_status();
+    });
+}
+
+}  // namespace
+
+// Tiles of 128 rows where they fill the card's 256 CUs, else of 32; where
+// even those leave it idle, the keys are split until 512 workgroups are
+// there or a workgroup is down to two key tiles.
+AttnPlan attn_plan(const AttnParams& a)
+{
+    AttnPlan p{};
+    const int64_t heads = (int64_t)a.B * a.Hkv;
+    p.waves = heads * ceil_div(a.rows, 128) >= 256 ? 4 : 1;
+    p.tiles = ceil_div(a.rows, p.waves * 32);
+    const int64_t groups = heads * p.tiles;
+    const int64_t keys = std::min<int64_t>((int64_t)a.window + p.waves * 32 / a.G, a.Lk) + std::min(a.sinks, a.Lk);
+    const int64_t most = std::max<int64_t>(1, keys / (2 * kKeyTile));
+    p.nsplit = groups >= 512 ? 1 : (int)std::min<int64_t>(most, (512 + groups - 1) / groups);
+    p.ws_bytes = p.nsplit > 1 ? (size_t)p.nsplit * heads * a.rows * (a.D + 2) * 4 : 0;
+    return p;
+}
+
+int launch_attn_fwd(AttnParams a, const AttnPlan& plan, bool bf, hipStream_t st)
+{
+    a.tiles = plan.tiles;
+    a.nsplit = plan.nsplit;
+    int rc;
+    if (plan.waves == 4) rc = bf ? run<true, 4>(a, st) : run<false, 4>(a, st);
+    else rc = bf ? run<true, 1>(a, st) : run<false, 1>(a, st);
+    if (rc != 0 || a.nsplit == 1) return rc;
+    const int lanes = a.D / 4, per = 256 / lanes;
+    const int64_t all = (int64_t)a.B * a.Hkv * a.rows;
+    const unsigned grid = (unsigned)((all + per - 1) / per);
+    if (bf) attn_join_kernel<true><<<grid, 256, 0, st>>>(a, lanes);
+    else attn_join_kernel<false><<<grid, 256, 0, st>>>(a, lanes);
+    return launch_status();
+}
+
+}  // namespace seq
+}  // namespace im2win

@@ -1,0 +1,168 @@
+// Shared helpers of the sequence operators' kernels (gfx950).
+//
+// Tiles of 16-bit tensors lie in LDS row by row (row = token), a row of
+// 64 or 128 elements (the head size rounded up) in 16-byte chunks. Chunk c of
+// row r is kept at position c ^ swz(r), so that both ways of reading are free
+// of bank conflicts: 16 rows at one chunk (a matrix operand whose rows are
+// tokens) and 4 rows at 4 neighbouring chunks (the transposed read, whose
+// rows are dimensions).
+//
+// Operand layouts of v_mfma_f32_32x32x16: lane l (half h = l / 32) holds row
+// or column l % 32 and the 8 depths "8h .. 8h+7" in order. The order of the
+// depths is free as long as both operands agree. The result has column
+// l % 32 and, in register i, row 8 * (i / 4) + 4 * h + i % 4. So 8 result
+// registers of one product, rounded and packed, are an operand of the next
+// whose depth order is: registers 8s .. 8s+7 of half h are the depths
+// 16s + 4h + {0..3} and 16s + 8 + 4h + {0..3}.
+#pragma once
+
+#include "common.hpp"
+
+namespace im2win {
+namespace seq {
+
+typedef unsigned int u32;
+typedef short short4_t __attribute__((ext_vector_type(4)));
+typedef short short8_t __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
+typedef float floatx2_t __attribute__((ext_vector_type(2)));
+typedef u32 u32x4_t __attribute__((ext_vector_type(4)));
+typedef u32 u32x2_t __attribute__((ext_vector_type(2)));
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// Rounds two floats to the element type (nearest even) in one register.
+template <bool BF>
+__device__ __forceinline__ u32 pack2(float a, float b)
+{
+    floatx2_t f = {a, b};
+    if constexpr (BF) return __builtin_bit_cast(u32, __builtin_convertvector(f, bf16x2_t));
+    else return __builtin_bit_cast(u32, __builtin_convertvector(f, half2_t));
+}
+
+// The two elements of a register as floats.
+template <bool BF>
+__device__ __forceinline__ floatx2_t unpack2(u32 v)
+{
+    if constexpr (BF) {
+        floatx2_t r = {__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)};
+        return r;
+    } else {
+        return __builtin_convertvector(__builtin_bit_cast(half2_t, v), floatx2_t);
+    }
+}
+
+template <bool BF>
+__device__ __forceinline__ floatx16_t mfma(u32x4_t a, u32x4_t b, floatx16_t c)
+{
+    if constexpr (BF)
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                       __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8_t, a),
+                                                      __builtin_bit_cast(half8_t, b), c, 0, 0, 0);
+}
+
+// 16 bytes per lane from p into LDS at byte lds + 16 * lane (lds the same for
+// the wave; M0 restored). Counts in vmcnt.
+__device__ __forceinline__ void dma16(const void* p, u32 lds)
+{
+    u32 save;
+    asm volatile(
+        "s_mov_b32 %0, m0\n\t"
+        "s_mov_b32 m0, %1\n\t"
+        "s_nop 0\n\t"
+        "global_load_lds_dwordx4 %2, off\n\t"
+        "s_mov_b32 m0, %0"
+        : "=&s"(save)
+        : "s"(lds), "v"(p)
+        : "memory");
+}
+
+// All of this wave's loads into LDS have arrived, its LDS reads are done, and
+// every wave of the workgroup has come here.
+__device__ __forceinline__ void sync_all()
+{
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// Elements of an LDS row for a head size padded to DP.
+__host__ __device__ constexpr int row_pitch(int DP) { return DP <= 64 ? 64 : 128; }
+
+template <int LP>
+__device__ __forceinline__ u32 swz(u32 row)
+{
+    if constexpr (LP == 128) return ((row & 3) << 2) | ((row >> 2) & 3);
+    else return ((row & 2) << 1) | ((row >> 2) & 3);
+}
+
+// Byte offset of element (row, col) in a tile.
+template <int LP>
+__device__ __forceinline__ u32 tile_at(u32 row, u32 col)
+{
+    return row * (LP * 2) + (((col >> 3) ^ swz<LP>(row)) << 4) + (col & 7) * 2;
+}
+
+typedef __attribute__((address_space(3))) unsigned char lds_byte;
+
+__device__ __forceinline__ u32x4_t lds_read16(u32 at)
+{
+    return *(__attribute__((address_space(3))) const u32x4_t*)(uintptr_t)at;
+}
+
+// Depths d0 + 8h .. + 7 of row `row`: an operand whose rows are tokens.
+template <int LP>
+__device__ __forceinline__ u32x4_t read_rows(u32 tile, u32 row, u32 col)
+{
+    return lds_read16(tile + tile_at<LP>(row, col));
+}
+
+// Transposed read: the operand whose row is dimension c0 + (lane % 32) and
+// whose depths are the tokens r0 + 4h + {0..3} and r0 + 8 + 4h + {0..3}.
+// ds_read_b64_tr_b16 turns, for each 16 lanes, 4 rows of 16 elements (lane i
+// points at 4 elements: row i / 4, elements 4 * (i % 4)) into 16 columns of 4.
+// PI: dimension of operand row 16g + 4a + b is 16g' + ... with the 4-groups
+// ordered so that result rows (see above) read 8 dimensions in order.
+template <int LP, bool PI = false>
+__device__ __forceinline__ u32x4_t read_cols(u32 tile, u32 r0, u32 c0)
+{
+    const u32 lane = threadIdx.x & 63;
+    const u32 h = lane >> 5, i = lane & 15, half16 = (lane >> 4) & 1;
+    const u32 row = r0 + 4 * h + (i >> 2);
+    u32 g4 = half16 * 4 + (i & 3);  // 4-group of dimensions, 0..7 in the block of 32
+    if constexpr (PI) g4 = (g4 & 4) | ((g4 & 1) << 1) | ((g4 >> 1) & 1);
+    const u32 col = c0 + 4 * g4;
+    typedef __attribute__((address_space(3))) short4_t* ptr;
+    const short4_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ptr)(uintptr_t)(tile + tile_at<LP>(row, col)));
+    const short4_t b =
+        __builtin_amdgcn_ds_read_tr16_b64_v4i16((ptr)(uintptr_t)(tile + tile_at<LP>(row + 8, col)));
+    u32x4_t r;
+    const u32x2_t ua = __builtin_bit_cast(u32x2_t, a), ub = __builtin_bit_cast(u32x2_t, b);
+    r.x = ua.x, r.y = ua.y, r.z = ub.x, r.w = ub.y;
+    return r;
+}
+
+// Sum and maximum over a lane and the lane 32 away.
+__device__ __forceinline__ float half_sum(float v)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float half_max(float v)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+// Blocks that absent rows are read from: zeros, and NaN for a bad page.
+struct Absent {
+    u32 zero[4];
+    u32 nan[4];
+};
+static __device__ const Absent kAbsent = {{0, 0, 0, 0}, {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu}};
+
+}  // namespace seq
+}  // namespace im2win

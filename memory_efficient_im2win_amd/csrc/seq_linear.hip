@@ -1,0 +1,373 @@
+// Linear attention with a decay a = exp(g) for each head, as one recurrence
+//     S_t = a S_(t-1) + k_t v_t^T,    out_t = w q_t S_t
+// over chunks of 32 tokens. With T the state before a chunk,
+//     out_i = a^(i+1) q_i T + sum_(j<=i) a^(i-j) (q_i . k_j) v_j,
+//     T'    = a^32 T + sum_j a^(31-j) k_j v_j^T,
+// all of them products on the matrix cores. The gradients are recurrences of
+// the same form: dq from (dout, v, k), and, over the tokens in reverse, dk
+// from (v, dout, q) and dv from (k, q, dout). In reverse the state given is
+// the gradient of the last state, which counts undecayed at the last token:
+// there (lead = 0) the state carried is a times the sum so far,
+//     out_i = a^i q_i T + ...,   T' = a^32 T + sum_j a^(32-j) k_j v_j^T.
+//
+// A long axis is cut into segments that run side by side: first each
+// segment's own state from zero, then the states before each segment (one
+// pass over them), then the outputs.
+//
+// A workgroup owns one segment of one head; a wave owns 32 columns (dv) of the
+// state, in fp32 registers for the whole walk, laid out as an operand:
+// register 8s+j of block mt in half h is row (dk) 32mt + 16s + 8h + j.
+//
+// Roundings to the element type: the chunk's decayed products q k^T, the state
+// as q's operand, and v times its decay. The first two enter only `out`,
+// which is rounded to the same type. Decayed values enter the state, so they
+// are split into a sum of parts of the type (bf16: 3 parts, 24 bits; fp16: 2,
+// 22 bits) wherever the state goes on to another segment or to the caller.
+#include "seq_common.hpp"
+#include "seq_kernels.hpp"
+
+namespace im2win {
+namespace seq {
+namespace {
+
+constexpr int kChunk = 32;
+
+enum Mode { kStates, kOutputs, kWhole };
+
+// Position of token t of the walk; absent tokens (t >= n) keep their place.
+__device__ __forceinline__ int walk(int t, int n, bool reverse) { return reverse && t < n ? n - 1 - t : t; }
+
+// Copies 32 tokens of x from walk position t0 into the LDS tile.
+template <int LP, int NW>
+__device__ __forceinline__ void stage_tokens(const Tensor& x, int b, int hd, int d, int t0, int n, bool reverse,
+                                             u32 lds)
+{
+    constexpr int CH = LP / 8, RPI = 64 / CH, N = kChunk / RPI;
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+#pragma unroll
+    for (int j = 0; j < (N + NW - 1) / NW; ++j) {
+        const int part = j * NW + wave;
+        if (N % NW != 0 && part >= N) break;
+        const u32 row = part * RPI + lane / CH;
+        const u32 c = (lane % CH) ^ swz<LP>(row);
+        const int t = t0 + (int)row;
+        const unsigned char* p = (const unsigned char*)kAbsent.zero;
+        if (t < n && (int)c * 8 < d) p = x.p + b * x.sb + walk(t, n, reverse) * x.sl + hd * x.sh + c * 16;
+        dma16(p, lds + part * 1024);
+    }
+}
+
+// x times w in parts of the element type that sum to it.
+template <bool BF, int PARTS>
+__device__ __forceinline__ void split_parts(u32x4_t x, const float* w, u32x4_t* out)
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        floatx2_t f = unpack2<BF>(x[j]);
+        f[0] *= w[2 * j];
+        f[1] *= w[2 * j + 1];
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p) {
+            const u32 r = pack2<BF>(f[0], f[1]);
+            out[p][j] = r;
+            if (p + 1 < PARTS) {
+                const floatx2_t g = unpack2<BF>(r);
+                f[0] -= g[0];
+                f[1] -= g[1];
+            }
+        }
+    }
+}
+
+template <bool BF, int DKP, int DVP, int MODE>
+__global__ __launch_bounds__(DVP * 2, 2) void linear_kernel(const LinParams a)
+{
+    constexpr int NW = DVP / 32, LK = row_pitch(DKP), LV = row_pitch(DVP), KS = DKP / 16, MT = DKP / 32;
+    constexpr int TK = kChunk * LK * 2, TV = kChunk * LV * 2, OUT = MODE != kStates;
+    constexpr int BUF = TK + TV + OUT * TK;  // k, v, q
+    constexpr int PARTS = MODE == kOutputs ? 1 : BF ? 3 : 2;
+    __shared__ __align__(1024) unsigned char smem[2 * BUF];
+    const u32 lds = (u32)(uintptr_t)(lds_byte*)smem;
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), h = lane >> 5, col = lane & 31;
+
+    const int id = blockIdx.x;
+    const int seg = id % a.nseg, hd = id / a.nseg % a.H, b = id / a.nseg / a.H % a.B;
+    const LinJob& J = a.job[id / a.nseg / a.H / a.B];
+    const int n = uniform(a.lens ? min(max(a.lens[b], 0), a.L) : a.L);
+    const bool reverse = J.reverse;
+    const float g = fmaxf(a.log_decay[hd], -1e4f) * kLog2e;  // a^n is 0 for every n >= 1 below
+    const int t_begin = seg * a.seg_len, t_end = min(a.L, t_begin + a.seg_len), t_live = min(t_end, n);
+
+    const auto stage = [&](int t, u32 at) {
+        stage_tokens<LK, NW>(J.k, b, hd, J.dk, t, n, reverse, at);
+        stage_tokens<LV, NW>(J.v, b, hd, J.dv, t, n, reverse, at + TK);
+        if (OUT) stage_tokens<LK, NW>(J.q, b, hd, J.dk, t, n, reverse, at + TK + TV);
+    };
+    if (t_begin < t_live) stage(t_begin, lds);
+
+    // The state: from the workspace in register order, or the one given.
+    floatx16_t S[MT] = {};
+    float* seg_state = J.seg + (((int64_t)b * a.H + hd) * a.nseg + seg) * (DKP * DVP) + threadIdx.x;
+    const int64_t given = ((int64_t)b * a.H + hd) * J.dk * J.dv;
+    if (MODE == kOutputs) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) S[mt][i] = seg_state[(mt * 16 + i) * (NW * 64)];
+    } else if (MODE == kWhole && J.s_in) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int dk = 32 * mt + 16 * (i / 8) + 8 * h + i % 8, dv = wave * 32 + col;
+                if (dk < J.dk && dv < J.dv) S[mt][i] = J.s_in[given + (int64_t)dk * J.sk + (int64_t)dv * J.sv];
+            }
+    }
+
+    // Decays inside a chunk: between tokens, from the chunk's start, to its end.
+    float between[16], to_end[2][8];
+    float from_start = 0;
+    if (OUT) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int j = 8 * (i / 4) + 4 * h + i % 4;
+            between[i] = j <= col ? __builtin_amdgcn_exp2f(g * (float)(col - j)) * J.w_in : 0.0f;
+        }
+        from_start = __builtin_amdgcn_exp2f(g * (float)(col + J.lead)) * J.w_state;
+    }
+    const auto set_to_end = [&](int tokens) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int j = 16 * s + 8 * (e / 4) + 4 * h + e % 4;
+                to_end[s][e] = __builtin_amdgcn_exp2f(g * (float)max(tokens - J.lead - j, 0)) * J.w_new;
+            }
+    };
+    set_to_end(kChunk);
+
+    int t = t_begin;
+    for (int it = 0; t < t_live; t += kChunk, ++it) {
+        const u32 kt = lds + (it & 1) * BUF, vt = kt + TK, qt = vt + TV;
+        const int tokens = min(kChunk, t_live - t);
+        sync_all();
+        if (t + kChunk < t_live) stage(t + kChunk, lds + ((it + 1) & 1) * BUF);
+        if (tokens < kChunk) set_to_end(tokens);
+
+        u32x4_t v[2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) v[s] = read_cols<LV>(vt, s * 16, wave * 32);
+        if (OUT) {
+            u32x4_t q[KS];
+            floatx16_t sc = {}, o = {};
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                q[ks] = read_rows<LK>(qt, col, ks * 16 + h * 8);
+                sc = mfma<BF>(read_rows<LK>(kt, col, ks * 16 + h * 8), q[ks], sc);
+            }
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                u32x4_t sp;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    sp[j] = pack2<BF>(S[ks / 2][(ks % 2) * 8 + 2 * j], S[ks / 2][(ks % 2) * 8 + 2 * j + 1]);
+                o = mfma<BF>(sp, q[ks], o);
+            }
+            o *= from_start;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                u32x4_t p;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    p[j] = pack2<BF>(sc[8 * s + 2 * j] * between[8 * s + 2 * j],
+                                     sc[8 * s + 2 * j + 1] * between[8 * s + 2 * j + 1]);
+                o = mfma<BF>(v[s], p, o);
+            }
+            if (t + col < t_end) {
+                const bool there = t + col < n;
+                unsigned char* out = J.out.p + b * J.out.sb + walk(t + col, n, reverse) * J.out.sl + hd * J.out.sh;
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) {
+                    const int d = wave * 32 + 8 * (i / 4) + 4 * h;
+                    u32x2_t w = {pack2<BF>(o[i], o[i + 1]), pack2<BF>(o[i + 2], o[i + 3])};
+                    if (!there) w = (u32x2_t)(0u);
+                    if (d < J.dv) *(u32x2_t*)(out + d * 2) = w;
+                }
+            }
+        }
+        const float fall = __builtin_amdgcn_exp2f(g * (float)tokens);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) S[mt] *= fall;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            u32x4_t w[PARTS];
+            split_parts<BF, PARTS>(v[s], to_end[s], w);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                const u32x4_t k = read_cols<LK, true>(kt, s * 16, mt * 32);
+#pragma unroll
+                for (int p = 0; p < PARTS; ++p) S[mt] = mfma<BF>(k, w[p], S[mt]);
+            }
+        }
+    }
+
+    if (OUT) {  // tokens past the sequence
+        const int first = max(t, t_begin);
+        for (int at = first + wave; at < t_end; at += NW) {
+            unsigned char* out = J.out.p + b * J.out.sb + at * J.out.sl + hd * J.out.sh;
+            if (lane * 4 < J.dv) *(u32x2_t*)(out + lane * 8) = (u32x2_t)(0u);
+        }
+    }
+    if (MODE == kStates) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) seg_state[(mt * 16 + i) * (NW * 64)] = S[mt][i];
+    } else if (MODE == kWhole && J.s_out) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int dk = 32 * mt + 16 * (i / 8) + 8 * h + i % 8, dv = wave * 32 + col;
+                if (dk < J.dk && dv < J.dv) J.s_out[given + (int64_t)dk * J.sk + (int64_t)dv * J.sv] = S[mt][i];
+            }
+    }
+}
+
+// Turns each segment's own state into the state before it, and writes the
+// last one. A thread owns one element of one head's state.
+template <int DKP, int DVP>
+__global__ __launch_bounds__(256) void linear_join_kernel(const LinParams a)
+{
+    constexpr int PER = DKP * DVP;
+    const int block = blockIdx.x % (PER / 256), id = blockIdx.x / (PER / 256);
+    const int bh = id % (a.B * a.H), b = bh / a.H, hd = bh % a.H;
+    const LinJob& J = a.job[id / (a.B * a.H)];
+    const int e = block * 256 + threadIdx.x;
+    const int reg = e / (DVP * 2), th = e % (DVP * 2), lane = th & 63;
+    const int dk = 32 * (reg / 16) + 16 * (reg % 16 / 8) + 8 * (lane >> 5) + reg % 8, dv = th / 64 * 32 + (lane & 31);
+    const bool real = dk < J.dk && dv < J.dv;
+    const int64_t at = (int64_t)bh * J.dk * J.dv + (int64_t)dk * J.sk + (int64_t)dv * J.sv;
+    const int n = uniform(a.lens ? min(max(a.lens[b], 0), a.L) : a.L);
+    const float g = fmaxf(a.log_decay[hd], -1e4f) * kLog2e;
+    float T = real && J.s_in ? J.s_in[at] : 0.0f;
+    float* x = J.seg + (int64_t)bh * a.nseg * PER + e;
+    for (int s = 0; s < a.nseg; ++s, x += PER) {
+        const int tokens = min(max(n - s * a.seg_len, 0), a.seg_len);
+        const float own = *x;
+        *x = T;
+        T = fmaf(T, __builtin_amdgcn_exp2f(g * (float)tokens), own);
+    }
+    if (real && J.s_out) J.s_out[at] = T;
+}
+
+// One token: out = scale q (a S + k v^T), the state updated in place, all in
+// fp32. Bound by the state's bytes, read and written once. A workgroup owns
+// `cols` columns of one head's state; 4 columns a thread, rows side by side.
+template <bool BF>
+__global__ __launch_bounds__(256) void linear_step_kernel(const LinStep a, int cols, int blocks)
+{
+    __shared__ float qs[128], ks[128], sum[256 * 4];
+    const int bh = blockIdx.x / blocks, c0 = blockIdx.x % blocks * cols, b = bh / a.H, hd = bh % a.H;
+    const int cut = min(cols, a.dv - c0), width = cut / 4, step = 256 / width;
+    const int tr = threadIdx.x / width, tc = threadIdx.x % width * 4;
+    if (threadIdx.x < a.dk) {
+        const uint16_t uq = *(const uint16_t*)(a.q.p + b * a.q.sb + hd * a.q.sh + threadIdx.x * 2);
+        const uint16_t uk = *(const uint16_t*)(a.k.p + b * a.k.sb + hd * a.k.sh + threadIdx.x * 2);
+        qs[threadIdx.x] = unpack2<BF>(uq)[0];
+        ks[threadIdx.x] = unpack2<BF>(uk)[0];
+    }
+    const float fall = __builtin_amdgcn_exp2f(fmaxf(a.log_decay[hd], -1e4f) * kLog2e);
+    float* S = a.state + ((int64_t)bh * a.dk) * a.dv + c0 + tc;
+    floatx4_t acc = {0, 0, 0, 0}, v = {0, 0, 0, 0};
+    const bool on = tr < step;
+    if (on) {
+        const u32x2_t u = *(const u32x2_t*)(a.v.p + b * a.v.sb + hd * a.v.sh + (c0 + tc) * 2);
+        const floatx2_t lo = unpack2<BF>(u[0]), hi = unpack2<BF>(u[1]);
+        v[0] = lo[0], v[1] = lo[1], v[2] = hi[0], v[3] = hi[1];
+    }
+    __syncthreads();
+    if (on) {
+        constexpr int U = 8;
+        for (int r = tr; r < a.dk; r += step * U) {
+            floatx4_t x[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (r + u * step < a.dk) x[u] = *(const floatx4_t*)(S + (int64_t)(r + u * step) * a.dv);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int k = r + u * step;
+                if (k >= a.dk) break;
+                const floatx4_t y = x[u] * fall + v * ks[k];
+                *(floatx4_t*)(S + (int64_t)k * a.dv) = y;
+                acc += y * qs[k];
+            }
+        }
+        *(floatx4_t*)(sum + tr * cut + tc) = acc;
+    }
+    __syncthreads();
+    if (threadIdx.x < cut) {
+        float o = 0;
+        const int live = min(step, a.dk);
+        for (int r = 0; r < live; ++r) o += sum[r * cut + threadIdx.x];
+        const u32 w = pack2<BF>(o * a.scale, 0.0f);
+        *(uint16_t*)(a.out.p + b * a.out.sb + hd * a.out.sh + (c0 + threadIdx.x) * 2) = (uint16_t)w;
+    }
+}
+
+template <bool BF, int DKP, int DVP>
+int run(const LinParams& a, hipStream_t st)
+{
+    const unsigned heads = (unsigned)(a.jobs * a.B * a.H), grid = heads * (unsigned)a.nseg;
+    if (a.nseg == 1) {
+        linear_kernel<BF, DKP, DVP, kWhole><<<grid, DVP * 2, 0, st>>>(a);
+        return launch_status();
+    }
+    linear_kernel<BF, DKP, DVP, kStates><<<grid, DVP * 2, 0, st>>>(a);
+    linear_join_kernel<DKP, DVP><<<heads * (DKP * DVP / 256), 256, 0, st>>>(a);
+    linear_kernel<BF, DKP, DVP, kOutputs><<<grid, DVP * 2, 0, st>>>(a);
+    return launch_status();
+}
+
+}  // namespace
+
+// Segments of at least 64 tokens, until 512 workgroups are there.
+LinPlan lin_plan(int jobs, int B, int L, int H)
+{
+    LinPlan p;
+    const int64_t heads = (int64_t)jobs * B * H;
+    const int64_t want = std::min<int64_t>((512 + heads - 1) / heads, std::max(1, L / 64));
+    p.seg_len = std::max(1, ceil_div(ceil_div(L, (int)want), kChunk)) * kChunk;
+    p.nseg = std::max(1, ceil_div(L, p.seg_len));
+    return p;
+}
+
+size_t lin_seg_bytes(const LinPlan& p, int B, int H, int dk, int dv)
+{
+    if (p.nseg == 1) return 0;
+    const auto pad = [](int d) { return with_head(d, [](auto D) { return (int)D.value; }); };
+    return (size_t)B * H * p.nseg * pad(dk) * pad(dv) * 4;
+}
+
+int launch_linear(const LinParams& a, bool bf, hipStream_t st)
+{
+    return with_head(a.job[0].dk, [&](auto DK) {
+        return with_head(a.job[0].dv, [&](auto DV) {
+            return bf ? run<true, DK.value, DV.value>(a, st) : run<false, DK.value, DV.value>(a, st);
+        });
+    });
+}
+
+// Whole heads where they fill the card, else 32 columns a workgroup.
+int launch_linear_step(const LinStep& a, bool bf, hipStream_t st)
+{
+    const int64_t heads = (int64_t)a.B * a.H;
+    const int cols = heads >= 512 ? a.dv : std::min(a.dv, 32), blocks = ceil_div(a.dv, cols);
+    const unsigned grid = (unsigned)(heads * blocks);
+    if (bf) linear_step_kernel<true><<<grid, 256, 0, st>>>(a, cols, blocks);
+    else linear_step_kernel<false><<<grid, 256, 0, st>>>(a, cols, blocks);
+    return launch_status();
+}
+
+}  // namespace seq
+}  // namespace im2win
