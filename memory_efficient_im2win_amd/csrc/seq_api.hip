@@ -83,6 +83,8 @@ bool attn_params(const seq_attention* a, AttnParams* p)
     p->q = tensor(a->q), p->k = tensor(a->k), p->v = tensor(a->v), p->out = tensor(a->out);
     p->lse = a->lse, p->q_lens = a->q_lens, p->kv_lens = a->kv_lens;
     p->table = a->page_table, p->table_stride = a->table_stride;
+    p->short_rows = p->k.sl < (1 << 24) && p->v.sl < (1 << 24);
+    p->same_kv = p->k.sb == p->v.sb && p->k.sl == p->v.sl && p->k.sh == p->v.sh;
     return true;
 }
 

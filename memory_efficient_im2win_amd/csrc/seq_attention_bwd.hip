@@ -20,7 +20,7 @@ namespace im2win {
 namespace seq {
 namespace {
 
-constexpr int kRowTile = 64, kKeysPerGroup = 128;
+constexpr int kRowTile = 32, kKeysPerGroup = 64;
 
 // The factor that dS carries in a column. Its first value and, when the
 // products outgrow it, its next one bring the largest to 2^13 .. 2^14; they
@@ -81,53 +81,98 @@ __global__ __launch_bounds__(256) void attn_stat_kernel(const AttnParams a)
     }
 }
 
-// Copies rows rt .. rt+63 of q and dout and their statistics into LDS.
+// Copies tiles of 32 rows of q and dout and their statistics into LDS, the
+// rows in order from r0. Rows from r_end on arrive as zeros. The pointers move
+// from tile to tile, so that no row is divided by the group in the loop.
 template <int LP>
-__device__ __forceinline__ void stage_rows(const AttnParams& a, int b, int hk, int bh, int rt, int r_end,
-                                           u32 lds_q, u32 lds_d, u32 lds_s)
-{
-    constexpr int CH = LP / 8, RPI = 64 / CH, N = kRowTile / RPI / 4;
-    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-        const int part = j * 4 + wave;
-        const u32 row = part * RPI + lane / CH;
-        const u32 c = (lane % CH) ^ swz<LP>(row);
-        dma16(row_ptr(a, a.q, b, hk, rt + row, r_end, c * 8), lds_q + part * 1024);
-        dma16(row_ptr(a, a.dout, b, hk, rt + row, r_end, c * 8), lds_d + part * 1024);
-    }
-    if (wave == 0) {
-        // Lanes 0-15: 64 values of lse, 16-31: of D; the rest copy zeros.
-        const int64_t at = (int64_t)bh * a.stat_rows + rt + (lane & 15) * 4;
-        const void* src = lane < 16 ? (const void*)(a.stat_lse + at)
-                        : lane < 32 ? (const void*)(a.stat_delta + at) : (const void*)kAbsent.zero;
-        dma16(src, lds_s);
-    }
-}
+struct RowStage {
+    static constexpr int CH = LP / 8, RPI = 64 / CH, N = kRowTile / RPI / 4, TILE = kRowTile * LP * 2;
+    const unsigned char *q[N], *d[N], *stat;
+    int g[N], r, r_end, G, step_g, lane, wave;
+    int64_t step_q, step_d, wrap_q, wrap_d;
+    bool in[N];
 
-// dK and dV of 128 keys, 32 a wave. Workgroups past the key tiles take the
-// chunks of sink rows.
+    __device__ __forceinline__ RowStage(const AttnParams& a, int b, int hk, int bh, int r0, int end)
+        : r_end(end), G(a.G), lane(threadIdx.x & 63), wave(uniform(threadIdx.x >> 6))
+    {
+        r = r0 + wave * RPI + lane / CH;
+        step_g = kRowTile % G;
+        step_q = kRowTile / G * a.q.sl + step_g * a.q.sh;
+        step_d = kRowTile / G * a.dout.sl + step_g * a.dout.sh;
+        wrap_q = a.q.sl - G * a.q.sh;
+        wrap_d = a.dout.sl - G * a.dout.sh;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int rj = r + j * 4 * RPI, i = a.by_group.div(rj), c = (lane % CH) ^ swz<LP>((j * 4 + wave) * RPI + lane / CH);
+            g[j] = rj - i * G;
+            in[j] = c * 8 < a.D;
+            const int64_t head = hk * G + g[j];
+            q[j] = a.q.p + b * a.q.sb + i * a.q.sl + head * a.q.sh + c * 16;
+            d[j] = a.dout.p + b * a.dout.sb + i * a.dout.sl + head * a.dout.sh + c * 16;
+        }
+        // Lanes 0-7: 32 values of lse, 8-15: of D; the rest copy the same.
+        const int64_t at = (int64_t)bh * a.stat_rows + r0 + (lane & 7) * 4;
+        stat = (const unsigned char*)((lane & 8 ? a.stat_delta : a.stat_lse) + at);
+    }
+    // The next tile, to lds (q), lds + TILE (dout), lds + 2 * TILE (statistics).
+    __device__ __forceinline__ void copy(u32 lds)
+    {
+        const unsigned char* zero = (const unsigned char*)kAbsent.zero;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const u32 at = lds + (j * 4 + wave) * 1024;
+            const bool there = r + j * 4 * RPI < r_end && in[j];
+            dma16(there ? q[j] : zero, at);
+            dma16(there ? d[j] : zero, at + TILE);
+            g[j] += step_g;
+            const bool over = g[j] >= G;
+            g[j] -= over ? G : 0;
+            q[j] += step_q + (over ? wrap_q : 0);
+            d[j] += step_d + (over ? wrap_d : 0);
+        }
+        if (wave == 0) dma16(stat, lds + 2 * TILE);
+        stat += kRowTile * 4;
+        r += kRowTile;
+    }
+};
+
+// dK and dV of 64 keys. Two waves share 32 keys: one forms S and P and sums dV,
+// the other, a row tile behind, forms dP and dS from the first one's P (handed
+// over in LDS, in fp32) and sums dK. Each holds 64 sums and 32 operand
+// registers for a head of 128, which leaves room to read ahead from LDS; one
+// wave doing both had none, and took 405 us where this takes TODO.
+// Workgroups before the key tiles take the chunks of sink rows.
 template <bool BF, int DP>
-__global__ __launch_bounds__(256, 1) void attn_dkv_kernel(const AttnParams a)
+__global__ __launch_bounds__(256, 2) void attn_dkv_kernel(const AttnParams a)
 {
     constexpr int LP = row_pitch(DP), KS = DP / 16, MT = DP / 32, TILE = kRowTile * LP * 2, STAT = 1024;
-    __shared__ __align__(1024) unsigned char smem[4 * TILE + 2 * STAT];
+    constexpr int BUF = 2 * TILE + STAT, HAND = 4096;  // row tiles of q and dout; P of 32 rows and keys
+    __shared__ __align__(1024) unsigned char smem[3 * BUF + 4 * HAND];
     const u32 lds = (u32)(uintptr_t)(lds_byte*)smem;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), h = lane >> 5;
+    const int block = wave >> 1;
+    const bool second = wave & 1;
+    const u32 hand = lds + 3 * BUF + block * (2 * HAND) + lane * 16;
 
-    const int items = a.key_tiles + a.sink_tiles * a.chunks;
-    const int id = (int)xcd_tile(blockIdx.x, gridDim.x, true);
-    const int item = id % items, bh = id / items, b = bh / a.Hkv, hk = bh % a.Hkv;
-    const bool extra = item >= a.key_tiles;
-    const int tile = extra ? (item - a.key_tiles) / a.chunks : item;
-    const int chunk = extra ? (item - a.key_tiles) % a.chunks : -1;
+    const int extras = a.sink_tiles * a.chunks, heads = a.B * a.Hkv;
+    int id = blockIdx.x, tile, chunk = -1, bh;
+    if (id < heads * extras) {
+        bh = id / extras;
+        tile = id % extras / a.chunks;
+        chunk = id % a.chunks;
+    } else {
+        id = (int)xcd_tile(id - heads * extras, gridDim.x - heads * extras, true);
+        bh = id / a.key_tiles;
+        tile = id % a.key_tiles;
+    }
+    const int b = bh / a.Hkv, hk = bh % a.Hkv;
     const Span s(a, b);
-    const int kg = tile * kKeysPerGroup, kw = kg + wave * 32, key = kw + (lane & 31);
+    const int kg = tile * kKeysPerGroup, kw = kg + block * 32, key = kw + (lane & 31);
 
     // Rows of this walk: positions p0 .. p1.
     const int last = min(kg + kKeysPerGroup, s.nk) - 1;
     int p0 = kg, p1 = (int)min((int64_t)last + a.window - 1, (int64_t)s.nk - 1);
-    if (extra) {
+    if (chunk >= 0) {
         p0 = (int)min((int64_t)kg + kKeysPerGroup - 1 + a.window + (int64_t)chunk * a.chunk_len, (int64_t)s.nk);
         p1 = (int)min((int64_t)p0 + a.chunk_len - 1, (int64_t)s.nk - 1);
     }
@@ -138,149 +183,134 @@ __global__ __launch_bounds__(256, 1) void attn_dkv_kernel(const AttnParams a)
     const int r_end = last < kg || i1 < i0 ? 0 : (i1 + 1) * a.G;
     const int n = r_end > rt0 ? (r_end - rt0 + kRowTile - 1) / kRowTile : 0;
 
-    if (n > 0) stage_rows<LP>(a, b, hk, bh, rt0, r_end, lds, lds + TILE, lds + 4 * TILE);
-
-    u32x4_t kf[KS], vf[KS];
+    RowStage<LP> stage(a, b, hk, bh, rt0, r_end);
+    if (n > 0) stage.copy(lds);
+    const Tensor& mine = second ? a.v : a.k;
+    u32x4_t kv[KS];
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
         const int d = ks * 16 + h * 8;
-        const bool in = key < s.nk && d < a.D;
-        kf[ks] = *(const u32x4_t*)(in ? a.k.p + b * a.k.sb + key * a.k.sl + hk * a.k.sh + d * 2
-                                      : (const unsigned char*)kAbsent.zero);
-        vf[ks] = *(const u32x4_t*)(in ? a.v.p + b * a.v.sb + key * a.v.sl + hk * a.v.sh + d * 2
-                                      : (const unsigned char*)kAbsent.zero);
+        kv[ks] = *(const u32x4_t*)(key < s.nk && d < a.D ? mine.p + b * mine.sb + key * mine.sl + hk * mine.sh + d * 2
+                                                         : (const unsigned char*)kAbsent.zero);
     }
+    settle_loads();
     const float c = a.scale * kLog2e;
     constexpr float kLift = BF ? 0.0f : 14.0f;  // log2 of P's factor
     Lift<BF> lift;
-    floatx16_t dk[MT] = {}, dv[MT] = {};
-    for (int t = 0; t < n; ++t) {
-        const int rt = rt0 + t * kRowTile;
-        const u32 bq = lds + (t & 1) * (2 * TILE), bd = bq + TILE, bs = lds + 4 * TILE + (t & 1) * STAT;
+    floatx16_t acc[MT] = {};
+    int at = 0, before = 2;  // this tile's buffer, the last one's
+    for (int t = 0; t <= n; ++t) {
+        const int next = 3 - at - before;
         sync_all();
-        if (t + 1 < n) {
-            const u32 nq = lds + ((t + 1) & 1) * (2 * TILE);
-            stage_rows<LP>(a, b, hk, bh, rt + kRowTile, r_end, nq, nq + TILE, lds + 4 * TILE + ((t + 1) & 1) * STAT);
-        }
+        if (t + 1 < n) stage.copy(lds + next * BUF);
+        const int mt_ = second ? t - 1 : t;
+        const u32 buf = lds + (second ? before : at) * BUF;
+        const u32 to = hand + (mt_ & 1) * HAND;
+        before = at;
+        at = next;
+        if (mt_ < 0 || mt_ >= n) continue;
+        const int rt = rt0 + mt_ * kRowTile, rb = min(rt + kRowTile, r_end) - 1;
+        const int pa = s.off + (int)a.by_group.div(rt), pb = s.off + (int)a.by_group.div(rb);
+        // Nothing here is seen by these keys.
+        if (pb < kw || (pa - (kw + 31) >= a.window && kw >= a.sinks)) continue;
+        const u32 rows = buf + (second ? TILE : 0), cols = buf + (second ? 0 : TILE);
+        floatx16_t x = {};
 #pragma unroll
-        for (int sb = 0; sb < 2; ++sb) {
-            const int ra = rt + sb * 32, rb = min(ra + 31, r_end - 1);
-            if (ra >= r_end) continue;
-            const int pa = s.off + (int)a.by_group.div(ra), pb = s.off + (int)a.by_group.div(rb);
-            // Nothing here is seen by this wave's keys.
-            if (pb < kw || (pa - (kw + 31) >= a.window && kw >= a.sinks)) continue;
-            floatx16_t sc = {}, dp = {};
+        for (int ks = 0; ks < KS; ++ks) x = mfma<BF>(read_rows<LP>(rows, lane & 31, ks * 16 + h * 8), kv[ks], x);
+        read_ahead<KS, 1, 4>();
+        const u32 stat = buf + 2 * TILE + (second ? 128 : 0) + 16 * h;
+        floatx4_t st[4];
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                sc = mfma<BF>(read_rows<LP>(bq, sb * 32 + (lane & 31), ks * 16 + h * 8), kf[ks], sc);
-                dp = mfma<BF>(read_rows<LP>(bd, sb * 32 + (lane & 31), ks * 16 + h * 8), vf[ks], dp);
-            }
-            floatx4_t l2[4], dl[4];
+        for (int g = 0; g < 4; ++g) st[g] = __builtin_bit_cast(floatx4_t, lds_read16(stat + 32 * g));
+        if (!second) {
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const u32 at = bs + (sb * 32 + 8 * g + 4 * h) * 4;
-                l2[g] = __builtin_bit_cast(floatx4_t, lds_read16(at));
-                dl[g] = __builtin_bit_cast(floatx4_t, lds_read16(at + 256));
-            }
-            const bool whole = pa >= kw + 31 && pb - kw < a.window && ra >= r_first && ra + 31 < r_end;
-            if (!whole) {
+            for (int i = 0; i < 16; ++i) x[i] = fmaf(x[i], c, kLift - st[i / 4][i % 4]);
+            if (!(pa >= kw + 31 && pb - kw < a.window && rt >= r_first && rt + kRowTile <= r_end)) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const int r = ra + 8 * (i / 4) + 4 * h + i % 4, p = s.off + (int)a.by_group.div(r);
-                    const bool seen = r >= r_first && r < r_end && key <= p &&
-                                      (p - key < a.window || key < a.sinks);
-                    l2[i / 4][i % 4] = seen ? l2[i / 4][i % 4] : INFINITY;
+                    const int r = rt + 8 * (i / 4) + 4 * h + i % 4, p = s.off + (int)a.by_group.div(r);
+                    const bool seen = r >= r_first && r < r_end && key <= p && (p - key < a.window || key < a.sinks);
+                    x[i] = seen ? x[i] : -INFINITY;
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 16; ++i) dp[i] -= dl[i / 4][i % 4];
+            for (int i = 0; i < 16; ++i) x[i] = __builtin_amdgcn_exp2f(x[i]);
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const floatx4_t y = {x[4 * g], x[4 * g + 1], x[4 * g + 2], x[4 * g + 3]};
+                lds_write16(to + g * 1024, __builtin_bit_cast(u32x4_t, y));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] -= st[i / 4][i % 4];
             if (!BF) {
                 float top = 0;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(dp[i]));
-                lift.update(top, dk);
-            }
-            const float ld = BF ? 1.0f : lift.in() * 0x1p-14f;
-            u32x4_t pr[2], ds[2];
+                for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(x[i]));
+                lift.update(top, acc);
+                const float ld = lift.in() * 0x1p-14f;
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-                float e[2], f[2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    e[j] = __builtin_amdgcn_exp2f(fmaf(sc[i + j], c, kLift - l2[i / 4][i % 4 + j]));
-                    f[j] = e[j] * (BF ? dp[i + j] : dp[i + j] * ld);
-                }
-                pr[i / 8][i % 8 / 2] = pack2<BF>(e[0], e[1]);
-                ds[i / 8][i % 8 / 2] = pack2<BF>(f[0], f[1]);
+                for (int i = 0; i < 16; ++i) x[i] *= ld;
             }
 #pragma unroll
-            for (int s2 = 0; s2 < 2; ++s2)
+            for (int g = 0; g < 4; ++g) {
+                const floatx4_t y = __builtin_bit_cast(floatx4_t, lds_read16(to + g * 1024));
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    dv[mt] = mfma<BF>(read_cols<LP>(bd, sb * 32 + s2 * 16, mt * 32), pr[s2], dv[mt]);
-                    dk[mt] = mfma<BF>(read_cols<LP>(bq, sb * 32 + s2 * 16, mt * 32), ds[s2], dk[mt]);
-                }
+                for (int i = 0; i < 4; ++i) x[4 * g + i] *= y[i];
+            }
         }
+        u32x4_t op[2];
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) op[i / 8][i % 8 / 2] = pack2<BF>(x[i], x[i + 1]);
+#pragma unroll
+        for (int s2 = 0; s2 < 2; ++s2)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) acc[mt] = mfma<BF>(read_cols<LP>(cols, s2 * 16, mt * 32), op[s2], acc[mt]);
+        read_ahead<2 * MT, 2, MT>();
     }
 
-    if (!BF) {
-        const float f = lift.out();
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            dk[mt] *= f;
-            dv[mt] *= 0x1p-14f;
-        }
-    }
-    if (tile < a.sink_tiles) {
-        // [sequence and head][sink tile][1 + chunks][dk, dv][key][D]
-        float* w = a.part + ((((int64_t)bh * a.sink_tiles + tile) * (a.chunks + 1) + chunk + 1) * 2 * kKeysPerGroup +
-                             wave * 32 + (lane & 31)) * a.D;
+    float f = second ? lift.out() : BF ? 1.0f : 0x1p-14f;
+    if (a.chunks && key < a.sinks) {
+        // [sequence and head][1 + chunks][dk, dv][key][D]
+        float* w = a.part + ((((int64_t)bh * (a.chunks + 1) + chunk + 1) * 2 + !second) * a.sinks + key) * a.D;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int j = 0; j < 16; j += 4) {
                 const int d = mt * 32 + 8 * (j / 4) + 4 * h;
-                if (d >= a.D) continue;
-                const floatx4_t x = {dk[mt][j], dk[mt][j + 1], dk[mt][j + 2], dk[mt][j + 3]};
-                const floatx4_t y = {dv[mt][j], dv[mt][j + 1], dv[mt][j + 2], dv[mt][j + 3]};
-                *(floatx4_t*)(w + d) = x;
-                *(floatx4_t*)(w + kKeysPerGroup * a.D + d) = y;
+                const floatx4_t y = {acc[mt][j] * f, acc[mt][j + 1] * f, acc[mt][j + 2] * f, acc[mt][j + 3] * f};
+                if (d < a.D) *(floatx4_t*)(w + d) = y;
             }
         return;
     }
-    if (key >= a.Lk) return;
-    unsigned char* ok = a.dk.p + b * a.dk.sb + key * a.dk.sl + hk * a.dk.sh;
-    unsigned char* ov = a.dv.p + b * a.dv.sb + key * a.dv.sl + hk * a.dv.sh;
+    if (key >= a.Lk || chunk >= 0) return;
+    if (second) f *= a.scale;
+    const Tensor& to = second ? a.dk : a.dv;
+    unsigned char* out = to.p + b * to.sb + key * to.sl + hk * to.sh;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int j = 0; j < 16; j += 4) {
             const int d = mt * 32 + 8 * (j / 4) + 4 * h;
-            if (d >= a.D) continue;
-            const u32x2_t x = {pack2<BF>(dk[mt][j] * a.scale, dk[mt][j + 1] * a.scale),
-                               pack2<BF>(dk[mt][j + 2] * a.scale, dk[mt][j + 3] * a.scale)};
-            const u32x2_t y = {pack2<BF>(dv[mt][j], dv[mt][j + 1]), pack2<BF>(dv[mt][j + 2], dv[mt][j + 3])};
-            *(u32x2_t*)(ok + d * 2) = x;
-            *(u32x2_t*)(ov + d * 2) = y;
+            const u32x2_t y = {pack2<BF>(acc[mt][j] * f, acc[mt][j + 1] * f),
+                               pack2<BF>(acc[mt][j + 2] * f, acc[mt][j + 3] * f)};
+            if (d < a.D) *(u32x2_t*)(out + d * 2) = y;
         }
 }
 
-// Sums a sink tile's parts in order. A quarter of D lanes hold a key.
+// Sums a sink key's parts in order. A quarter of D lanes hold a key.
 template <bool BF>
 __global__ __launch_bounds__(256) void attn_sink_join_kernel(const AttnParams a, int lanes)
 {
     const int per = 256 / lanes, sub = threadIdx.x / lanes, d = threadIdx.x % lanes * 4;
     const int64_t at = (int64_t)blockIdx.x * per + sub;
-    const int which = (int)(at & 1), k = (int)(at >> 1) % kKeysPerGroup;
-    const int64_t bt = (at >> 1) / kKeysPerGroup;
-    const int tile = (int)(bt % a.sink_tiles);
-    const int64_t bh = bt / a.sink_tiles;
-    const int key = tile * kKeysPerGroup + k;
-    if (sub >= per || bh >= (int64_t)a.B * a.Hkv || d >= a.D || key >= a.Lk) return;
+    const int which = (int)(at & 1), key = (int)((at >> 1) % a.sinks);
+    const int64_t bh = (at >> 1) / a.sinks;
+    if (sub >= per || bh >= (int64_t)a.B * a.Hkv || d >= a.D) return;
     const int b = (int)(bh / a.Hkv), hk = (int)(bh % a.Hkv);
     floatx4_t x = {0, 0, 0, 0};
     for (int c = 0; c <= a.chunks; ++c)
-        x += *(const floatx4_t*)(a.part + (((bt * (a.chunks + 1) + c) * 2 + which) * kKeysPerGroup + k) * a.D + d);
+        x += *(const floatx4_t*)(a.part + (((bh * (a.chunks + 1) + c) * 2 + which) * a.sinks + key) * a.D + d);
     if (!which) x *= a.scale;
     const Tensor& t = which ? a.dv : a.dk;
     const u32x2_t w = {pack2<BF>(x[0], x[1]), pack2<BF>(x[2], x[3])};
@@ -305,7 +335,9 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnParams a)
     const int pw_lo = s.off + (int)a.by_group.div(rw), pw_hi = s.off + min((int)a.by_group.div(rw + 31), s.nq - 1);
     const int p = s.off + (int)a.by_group.div(r);
 
-    if (kt.n > 0) stage_keys<LP, NW>(a, a.k, a.v, b, hk, kt, kt.at(0), lds, lds + TILE);
+    KeyStage<LP, NW> stage(a, kt, b, hk);
+    stage.clear(lds, 4 * TILE, a.D);
+    if (kt.n > 0) stage.copy(kt.at(0), lds);
 
     u32x4_t q[KS], dout[KS];
 #pragma unroll
@@ -319,13 +351,14 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnParams a)
         delta = a.stat_delta[(int64_t)bh * a.stat_rows + r];
     }
     const float c = a.scale * kLog2e;
+    settle_loads();
 
     Lift<BF> lift;
     floatx16_t dq[MT] = {};
     for (int it = 0; it < kt.n; ++it) {
         const u32 buf = lds + (it & 1) * (2 * TILE), nbuf = lds + ((it + 1) & 1) * (2 * TILE);
         sync_all();
-        if (it + 1 < kt.n) stage_keys<LP, NW>(a, a.k, a.v, b, hk, kt, kt.at(it + 1), nbuf, nbuf + TILE);
+        if (it + 1 < kt.n) stage.copy(kt.at(it + 1), nbuf);
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
             const int k0 = kt.at(it) * kKeyTile + kb * 32;
@@ -336,6 +369,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnParams a)
                 sc = mfma<BF>(read_rows<LP>(buf, kb * 32 + (lane & 31), ks * 16 + h * 8), q[ks], sc);
                 dp = mfma<BF>(read_rows<LP>(buf + TILE, kb * 32 + (lane & 31), ks * 16 + h * 8), dout[ks], dp);
             }
+            read_ahead<2 * KS, 1, 4>();
 #pragma unroll
             for (int i = 0; i < 16; ++i) sc[i] = fmaf(sc[i], c, -l2);
             if (k0 + 31 > pw_lo || k0 <= pw_hi - a.window) {
@@ -367,6 +401,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnParams a)
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
                     dq[mt] = mfma<BF>(read_cols<LP>(buf, kb * 32 + s2 * 16, mt * 32), ds[s2], dq[mt]);
+            read_ahead<2 * MT, 2, MT>();
         }
     }
     if (r >= a.rows) return;
@@ -401,31 +436,37 @@ int run(AttnParams a, hipStream_t st)
     });
     if (rc != 0 || a.sink_tiles == 0) return rc;
     const int lanes = a.D / 4, per = 256 / lanes;
-    const int64_t all = heads * a.sink_tiles * kKeysPerGroup * 2;
+    const int64_t all = heads * a.sinks * 2;
     attn_sink_join_kernel<BF><<<(unsigned)((all + per - 1) / per), 256, 0, st>>>(a, lanes);
     return launch_status();
 }
 
 }  // namespace
 
-// Sink keys' rows past the window are cut into chunks as long as the window's
-// own walk, so that no workgroup walks much longer than the others.
+// Sink keys' rows past the window are cut into chunks of about 512 flattened
+// rows, so that they are spread over the card, as long as that makes no more
+// than 256 workgroups; no chunk walks further than the window's own walk
+// unless the partial sums would pass 2^30 bytes.
 AttnBwdPlan attn_bwd_plan(const AttnParams& a)
 {
     AttnBwdPlan p{};
     p.stat_rows = ceil_div(a.rows, kRowTile) * kRowTile + kRowTile;
     p.key_tiles = ceil_div(a.Lk, kKeysPerGroup);
-    p.chunk_len = (int)std::min<int64_t>((int64_t)a.window + kKeysPerGroup, a.Lk);
     // Positions past the first key tile's window, if any key there is a sink.
     const int64_t past = (int64_t)a.Lk - (kKeysPerGroup - 1) - a.window;
+    const int64_t heads = (int64_t)a.B * a.Hkv;
     if (a.sinks > 0 && past > 0) {
-        p.sink_tiles = ceil_div(std::min(a.sinks, a.Lk), kKeysPerGroup);
+        p.sink_tiles = ceil_div(a.sinks, kKeysPerGroup);
+        const int64_t fine = ceil_div(512, a.G), own = (int64_t)a.window + kKeysPerGroup;
+        int64_t chunks = std::min((past + fine - 1) / fine, std::max<int64_t>(1, 256 / (heads * p.sink_tiles)));
+        chunks = std::max(chunks, (past + own - 1) / own);
+        chunks = std::max<int64_t>(1, std::min(chunks, (int64_t(1) << 27) / (heads * a.sinks * a.D)));
+        p.chunk_len = (int)((past + chunks - 1) / chunks);
         p.chunks = (int)((past + p.chunk_len - 1) / p.chunk_len);
     }
-    const size_t heads = (size_t)a.B * a.Hkv;
-    p.stat_bytes = heads * p.stat_rows * 4;
-    p.ws_bytes = 2 * p.stat_bytes +
-                 heads * p.sink_tiles * (p.chunks + 1) * 2 * kKeysPerGroup * (size_t)a.D * 4;
+    p.stat_bytes = (size_t)heads * p.stat_rows * 4;
+    p.ws_bytes = 2 * p.stat_bytes;
+    if (p.chunks) p.ws_bytes += (size_t)heads * (p.chunks + 1) * 2 * a.sinks * a.D * 4;
     return p;
 }
 

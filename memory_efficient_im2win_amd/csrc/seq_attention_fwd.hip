@@ -48,7 +48,13 @@ __global__ __launch_bounds__(NW * 64, NW > 2 ? 2 : 1) void attn_fwd_kernel(const
     const int pw_lo = s.off + (int)a.by_group.div(rw), pw_hi = s.off + min((int)a.by_group.div(rw + 31), s.nq - 1);
     const int p = s.off + (int)a.by_group.div(r);
 
-    if (it0 < it1) stage_keys<LP, NW>(a, a.k, a.v, b, hk, kt, kt.at(it0), lds, lds + TILE);
+    KeyStage<LP, NW> stage(a, kt, b, hk);
+    stage.clear(lds, 4 * TILE, a.D);
+    if (it0 < it1) {
+        stage.look_up(kt.at(it0));
+        stage.copy(kt.at(it0), lds);
+        if (it0 + 1 < it1) stage.look_up(kt.at(it0 + 1));
+    }
 
     // A negative scale flips the rows' sign (exact), so that the largest
     // product is the largest score; a zero one clears them.
@@ -61,13 +67,18 @@ __global__ __launch_bounds__(NW * 64, NW > 2 ? 2 : 1) void attn_fwd_kernel(const
         q[ks] = (q[ks] & keep) ^ flip;
     }
 
+    settle_loads();
+
     floatx16_t o[MT] = {};
     constexpr float kLift = BF ? 0.0f : 6.0f;
     float m = -INFINITY, mc = 0, l = 0;  // reference, the same in log2 units, this lane's sum
     for (int it = it0; it < it1; ++it) {
         const u32 buf = lds + ((it - it0) & 1) * (2 * TILE), nbuf = lds + ((it - it0 + 1) & 1) * (2 * TILE);
         sync_all();
-        if (it + 1 < it1) stage_keys<LP, NW>(a, a.k, a.v, b, hk, kt, kt.at(it + 1), nbuf, nbuf + TILE);
+        if (it + 1 < it1) {
+            stage.copy(kt.at(it + 1), nbuf);
+            if (it + 2 < it1) stage.look_up(kt.at(it + 2));
+        }
         const int k0 = kt.at(it) * kKeyTile;
         if (rw >= r_end || k0 > pw_hi || (k0 + kKeyTile - 1 <= pw_lo - a.window && k0 >= a.sinks)) continue;
 
@@ -77,6 +88,7 @@ __global__ __launch_bounds__(NW * 64, NW > 2 ? 2 : 1) void attn_fwd_kernel(const
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb)
                 sc[kb] = mfma<BF>(read_rows<LP>(buf, kb * 32 + (lane & 31), ks * 16 + h * 8), q[ks], sc[kb]);
+        read_ahead<2 * KS, 1, 6>();
         if (k0 + kKeyTile - 1 > pw_lo || k0 <= pw_hi - a.window) {
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb)
@@ -120,6 +132,7 @@ __global__ __launch_bounds__(NW * 64, NW > 2 ? 2 : 1) void attn_fwd_kernel(const
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
                 o[mt] = mfma<BF>(read_cols<LP>(buf + TILE, ks * 16, mt * 32), pr[ks], o[mt]);
+        read_ahead<4 * MT, 2, 4>();
     }
 
     if (r >= a.rows) return;

@@ -78,8 +78,42 @@ __device__ __forceinline__ void dma16(const void* p, u32 lds)
         "global_load_lds_dwordx4 %2, off\n\t"
         "s_mov_b32 m0, %0"
         : "=&s"(save)
-        : "s"(lds), "v"(p)
+        : "s"(uniform(lds)), "v"(p)
         : "memory");
+}
+
+// The same from a wave-uniform base and a lane offset.
+__device__ __forceinline__ void dma16(const void* base, u32 offset, u32 lds)
+{
+    u32 save;
+    asm volatile(
+        "s_mov_b32 %0, m0\n\t"
+        "s_mov_b32 m0, %1\n\t"
+        "s_nop 0\n\t"
+        "global_load_lds_dwordx4 %2, %3\n\t"
+        "s_mov_b32 m0, %0"
+        : "=&s"(save)
+        : "s"(uniform(lds)), "v"(offset), "s"(base)
+        : "memory");
+}
+
+// Waits for this wave's loads, visibly to the compiler: a load that it still
+// counts as pending when a loop begins makes it wait, on every turn of the
+// loop, for whatever copy into LDS was issued last.
+__device__ __forceinline__ void settle_loads() { __builtin_amdgcn_s_waitcnt(0x0f70); }
+
+// Orders a run of N products that each need PER reads from LDS: the reads of AHEAD products first, then a product and the reads of a
+// later one in turn.
+template <int N, int PER, int AHEAD>
+__device__ __forceinline__ void read_ahead()
+{
+    __builtin_amdgcn_sched_group_barrier(0x100, AHEAD * PER, 0);
+#pragma unroll
+    for (int i = 0; i < N - AHEAD; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, PER, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, AHEAD, 0);
 }
 
 // All of this wave's loads into LDS have arrived, its LDS reads are done, and
@@ -111,6 +145,11 @@ typedef __attribute__((address_space(3))) unsigned char lds_byte;
 __device__ __forceinline__ u32x4_t lds_read16(u32 at)
 {
     return *(__attribute__((address_space(3))) const u32x4_t*)(uintptr_t)at;
+}
+
+__device__ __forceinline__ void lds_write16(u32 at, u32x4_t v)
+{
+    *(__attribute__((address_space(3))) u32x4_t*)(uintptr_t)at = v;
 }
 
 // Depths d0 + 8h .. + 7 of row `row`: an operand whose rows are tokens.

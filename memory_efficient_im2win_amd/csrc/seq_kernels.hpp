@@ -33,6 +33,8 @@ struct AttnParams {
     int pages, window, sinks;
     float scale;
     FastDiv by_group, by_page;
+    bool short_rows;  // 32-bit offsets reach across a tile's keys
+    bool same_kv;     // k and v have the same strides
     // Forward: key tiles split over nsplit workgroups, partial results in ws.
     int nsplit, tiles;
     float* part;
