@@ -22,12 +22,13 @@ constexpr int64_t kGrid = 0x7fffffff;  // workgroups of a launch
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
-// A 16-bit tensor of `elems` elements: strides and base fit 16-byte accesses.
+// A 16-bit tensor of `elems` elements: strides and base fit 16-byte accesses,
+// and 32-bit offsets reach across a tile of tokens.
 bool good(const seq_tensor& t, int64_t elems)
 {
     if (elems == 0) return true;
     return t.p && aligned(t.p, 16) && t.stride_b >= 0 && t.stride_l >= 0 && t.stride_h >= 0 && t.stride_b % 8 == 0 &&
-           t.stride_l % 8 == 0 && t.stride_h % 8 == 0;
+           t.stride_l % 8 == 0 && t.stride_h % 8 == 0 && t.stride_l < (1 << 24);
 }
 
 bool good_head(int d) { return d >= 8 && d <= 128 && d % 8 == 0; }
@@ -83,8 +84,6 @@ bool attn_params(const seq_attention* a, AttnParams* p)
     p->q = tensor(a->q), p->k = tensor(a->k), p->v = tensor(a->v), p->out = tensor(a->out);
     p->lse = a->lse, p->q_lens = a->q_lens, p->kv_lens = a->kv_lens;
     p->table = a->page_table, p->table_stride = a->table_stride;
-    p->short_rows = p->k.sl < (1 << 24) && p->v.sl < (1 << 24);
-    p->same_kv = p->k.sb == p->v.sb && p->k.sl == p->v.sl && p->k.sh == p->v.sh;
     return true;
 }
 

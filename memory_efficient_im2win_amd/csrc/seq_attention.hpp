@@ -42,24 +42,36 @@ struct KeyTiles {
     __device__ __forceinline__ int at(int i) const { return i < far ? i : first + i - far; }
 };
 
-// Copies tiles of 64 keys and values into LDS (k at `lds`, v a tile later).
-// Keys that no row of the workgroup sees arrive as zeros, so what they hold in
-// memory does not matter; those of a page outside the pool as NaN. Chunks past
-// the head size are not written: clear() zeroes them once.
-template <int LP, int NW>
+// Whether the query at position p sees key k0 + i, for constants i: compares
+// with three numbers of the block. (Opaque: the compiler would otherwise keep
+// p - i for every i of a walk in registers.)
+struct Mask {
+    int near, edge, sink;
+    __device__ __forceinline__ Mask(int p, int k0, const AttnParams& a)
+        : near(p - k0), edge(near - a.window), sink(a.sinks - k0)
+    {
+        asm("" : "+v"(near), "+v"(edge), "+v"(sink));
+    }
+    __device__ __forceinline__ bool operator()(int i) const { return i <= near && (i > edge || i < sink); }
+};
+
+// Copies tiles of 64 keys or values into LDS. Keys that no row of the
+// workgroup sees arrive as zeros, so what they hold in memory does not matter;
+// those of a page outside the pool as NaN. Chunks past the head size are not
+// written: clear() zeroes them once.
+template <int LP, int NW, bool PAGED>
 struct KeyStage {
     static constexpr int CH = LP / 8, RPI = 64 / CH, N = kKeyTile / RPI / NW, TILE = kKeyTile * LP * 2;
+    struct Pages {
+        int id[N];
+    };
     const AttnParams& a;
     const KeyTiles& kt;
     int b, hk, lane, wave;
-    u32 ok, ov;     // lane offsets of the plain copy
-    int page[N];    // the next tile's pages (or the sequence)
 
     __device__ __forceinline__ KeyStage(const AttnParams& a_, const KeyTiles& kt_, int b_, int hk_)
         : a(a_), kt(kt_), b(b_), hk(hk_), lane(threadIdx.x & 63), wave(uniform(threadIdx.x >> 6))
     {
-        ok = (lane / CH) * (u32)a.k.sl;
-        ov = (lane / CH) * (u32)a.v.sl;
     }
     __device__ __forceinline__ u32 row(int j) const { return (j * NW + wave) * RPI + lane / CH; }
     __device__ __forceinline__ u32 chunk(int j) const { return (lane % CH) ^ swz<LP>(row(j)); }
@@ -72,56 +84,50 @@ struct KeyStage {
     }
 
     // Looks up tile t's pages, a tile ahead of their use.
-    __device__ __forceinline__ void look_up(int t)
+    __device__ __forceinline__ void look_up(int t, Pages& p) const
     {
-        if (!a.table) return;
+        if (!PAGED) return;
 #pragma unroll
         for (int j = 0; j < N; ++j)
-            page[j] = a.table[b * a.table_stride + a.by_page.div(min(t * kKeyTile + (int)row(j), kt.hi))];
+            p.id[j] = a.table[b * a.table_stride + a.by_page.div(min(t * kKeyTile + (int)row(j), kt.hi))];
     }
 
-    __device__ __forceinline__ void copy(int t, u32 lds)
+    // Tile t of x (k or v).
+    __device__ __forceinline__ void copy(const Tensor& x, int t, const Pages& p, u32 lds) const
     {
         const int k0 = t * kKeyTile;
-        if (!a.table && a.short_rows && k0 + kKeyTile - 1 <= kt.hi && (k0 >= kt.lo || k0 + kKeyTile <= a.sinks)) {
-            const unsigned char* pk = a.k.p + b * a.k.sb + hk * a.k.sh + (int64_t)k0 * a.k.sl;
-            const unsigned char* pv = a.v.p + b * a.v.sb + hk * a.v.sh + (int64_t)k0 * a.v.sl;
+        const unsigned char* const zero = (const unsigned char*)kAbsent.zero;
+        if constexpr (!PAGED) {
+            const unsigned char* from = x.p + b * x.sb + hk * x.sh + (k0 + wave * RPI) * x.sl;
+            const u32 row_at = (lane / CH) * (u32)x.sl;
+            if (k0 + kKeyTile - 1 <= kt.hi && (k0 >= kt.lo || k0 + kKeyTile <= a.sinks)) {
 #pragma unroll
-            for (int j = 0; j < N; ++j) {
-                const int part = j * NW + wave;
-                if ((int)chunk(j) * 8 < a.D) {
-                    dma16(pk + part * RPI * a.k.sl, ok + chunk(j) * 16, lds + part * 1024);
-                    dma16(pv + part * RPI * a.v.sl, ov + chunk(j) * 16, lds + TILE + part * 1024);
+                for (int j = 0; j < N; ++j)
+                    if ((int)chunk(j) * 8 < a.D)
+                        dma16(from + j * NW * RPI * x.sl, row_at + chunk(j) * 16, lds + (j * NW + wave) * 1024);
+            } else {
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    const int key = k0 + (int)row(j);
+                    const bool there = key <= kt.hi && (key >= kt.lo || key < a.sinks);
+                    if ((int)chunk(j) * 8 < a.D)
+                        dma16(there ? from + j * NW * RPI * x.sl + row_at + chunk(j) * 16 : zero,
+                              lds + (j * NW + wave) * 1024);
                 }
             }
             return;
         }
         // All pages at once, before copies are under way that a wait for one
         // of them would also wait for.
-        if (a.table) settle_loads();
+        settle_loads();
+        const unsigned char* from = x.p + hk * x.sh;
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            const int part = j * NW + wave, key = k0 + (int)row(j);
-            const unsigned char *pk = (const unsigned char*)kAbsent.zero, *pv = pk;
-            if (key <= kt.hi && (key >= kt.lo || key < a.sinks)) {
-                int at = key, pg = b;
-                if (a.table) {
-                    pg = page[j];
-                    at = key - (int)a.by_page.div(key) * (int)a.by_page.d;
-                }
-                if (a.table && (pg < 0 || pg >= a.pages)) {
-                    pk = pv = (const unsigned char*)kAbsent.nan;
-                } else {
-                    const int64_t in = (int64_t)hk * a.k.sh + chunk(j) * 16;
-                    pk = a.k.p + pg * a.k.sb + at * a.k.sl + in;
-                    pv = a.v.p + (a.same_kv ? pg * a.k.sb + at * a.k.sl + in
-                                            : pg * a.v.sb + at * a.v.sl + (int64_t)hk * a.v.sh + chunk(j) * 16);
-                }
-            }
-            if ((int)chunk(j) * 8 < a.D) {
-                dma16(pk, lds + part * 1024);
-                dma16(pv, lds + TILE + part * 1024);
-            }
+            const int key = k0 + (int)row(j), at = key - (int)a.by_page.div(key) * (int)a.by_page.d;
+            const unsigned char* e = from + p.id[j] * x.sb + at * x.sl + chunk(j) * 16;
+            if (p.id[j] < 0 || p.id[j] >= a.pages) e = (const unsigned char*)kAbsent.nan;
+            if (!(key <= kt.hi && (key >= kt.lo || key < a.sinks))) e = zero;
+            if ((int)chunk(j) * 8 < a.D) dma16(e, lds + (j * NW + wave) * 1024);
         }
     }
 };

@@ -20,7 +20,7 @@ namespace im2win {
 namespace seq {
 namespace {
 
-constexpr int kRowTile = 32, kKeysPerGroup = 64;
+constexpr int kRowTile = 32;
 
 // The factor that dS carries in a column. Its first value and, when the
 // products outgrow it, its next one bring the largest to 2^13 .. 2^14; they
@@ -84,10 +84,12 @@ __global__ __launch_bounds__(256) void attn_stat_kernel(const AttnParams a)
 // Copies tiles of 32 rows of q and dout and their statistics into LDS, the
 // rows in order from r0. Rows from r_end on arrive as zeros. The pointers move
 // from tile to tile, so that no row is divided by the group in the loop.
-template <int LP>
+template <int LP, int NW>
 struct RowStage {
-    static constexpr int CH = LP / 8, RPI = 64 / CH, N = kRowTile / RPI / 4, TILE = kRowTile * LP * 2;
-    const unsigned char *q[N], *d[N], *stat;
+    static constexpr int CH = LP / 8, RPI = 64 / CH, PARTS = kRowTile / RPI, N = (PARTS + NW - 1) / NW;
+    static constexpr int TILE = kRowTile * LP * 2;
+    const unsigned char *q[N], *d[N];
+    const float* stat;
     int g[N], r, r_end, G, step_g, lane, wave;
     int64_t step_q, step_d, wrap_q, wrap_d;
     bool in[N];
@@ -103,16 +105,16 @@ struct RowStage {
         wrap_d = a.dout.sl - G * a.dout.sh;
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            const int rj = r + j * 4 * RPI, i = a.by_group.div(rj), c = (lane % CH) ^ swz<LP>((j * 4 + wave) * RPI + lane / CH);
+            const int rj = r + j * NW * RPI, i = a.by_group.div(rj);
+            const int c = (lane % CH) ^ swz<LP>((j * NW + wave) * RPI + lane / CH);
             g[j] = rj - i * G;
             in[j] = c * 8 < a.D;
             const int64_t head = hk * G + g[j];
             q[j] = a.q.p + b * a.q.sb + i * a.q.sl + head * a.q.sh + c * 16;
             d[j] = a.dout.p + b * a.dout.sb + i * a.dout.sl + head * a.dout.sh + c * 16;
         }
-        // Lanes 0-7: 32 values of lse, 8-15: of D; the rest copy the same.
-        const int64_t at = (int64_t)bh * a.stat_rows + r0 + (lane & 7) * 4;
-        stat = (const unsigned char*)((lane & 8 ? a.stat_delta : a.stat_lse) + at);
+        // Lanes 0-7: 32 values of lse, 8-15: of D.
+        stat = (lane & 8 ? a.stat_delta : a.stat_lse) + (int64_t)bh * a.stat_rows + r0 + (lane & 7) * 4;
     }
     // The next tile, to lds (q), lds + TILE (dout), lds + 2 * TILE (statistics).
     __device__ __forceinline__ void copy(u32 lds)
@@ -120,8 +122,9 @@ struct RowStage {
         const unsigned char* zero = (const unsigned char*)kAbsent.zero;
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            const u32 at = lds + (j * 4 + wave) * 1024;
-            const bool there = r + j * 4 * RPI < r_end && in[j];
+            if (PARTS % NW != 0 && j * NW + wave >= PARTS) break;
+            const u32 at = lds + (j * NW + wave) * 1024;
+            const bool there = r + j * NW * RPI < r_end && in[j];
             dma16(there ? q[j] : zero, at);
             dma16(there ? d[j] : zero, at + TILE);
             g[j] += step_g;
@@ -130,24 +133,24 @@ struct RowStage {
             q[j] += step_q + (over ? wrap_q : 0);
             d[j] += step_d + (over ? wrap_d : 0);
         }
-        if (wave == 0) dma16(stat, lds + 2 * TILE);
-        stat += kRowTile * 4;
+        if (wave == NW - 1 && lane < 16) dma16(stat, lds + 2 * TILE);
+        stat += kRowTile;
         r += kRowTile;
     }
 };
 
-// dK and dV of 64 keys. Two waves share 32 keys: one forms S and P and sums dV,
+// dK and dV of NW * 16 keys. Two waves share 32 keys: one forms S and P and sums dV,
 // the other, a row tile behind, forms dP and dS from the first one's P (handed
 // over in LDS, in fp32) and sums dK. Each holds 64 sums and 32 operand
 // registers for a head of 128, which leaves room to read ahead from LDS; one
 // wave doing both had none, and took 405 us where this takes TODO.
 // Workgroups before the key tiles take the chunks of sink rows.
-template <bool BF, int DP>
-__global__ __launch_bounds__(256, 2) void attn_dkv_kernel(const AttnParams a)
+template <bool BF, int DP, int NW>
+__global__ __launch_bounds__(NW * 64, 2) void attn_dkv_kernel(const AttnParams a)
 {
     constexpr int LP = row_pitch(DP), KS = DP / 16, MT = DP / 32, TILE = kRowTile * LP * 2, STAT = 1024;
-    constexpr int BUF = 2 * TILE + STAT, HAND = 4096;  // row tiles of q and dout; P of 32 rows and keys
-    __shared__ __align__(1024) unsigned char smem[3 * BUF + 4 * HAND];
+    constexpr int KEYS = NW * 16, BUF = 2 * TILE + STAT, HAND = 4096;  // row tiles of q and dout; P of 32 rows and keys
+    __shared__ __align__(1024) unsigned char smem[3 * BUF + NW * HAND];
     const u32 lds = (u32)(uintptr_t)(lds_byte*)smem;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), h = lane >> 5;
     const int block = wave >> 1;
@@ -167,13 +170,13 @@ __global__ __launch_bounds__(256, 2) void attn_dkv_kernel(const AttnParams a)
     }
     const int b = bh / a.Hkv, hk = bh % a.Hkv;
     const Span s(a, b);
-    const int kg = tile * kKeysPerGroup, kw = kg + block * 32, key = kw + (lane & 31);
+    const int kg = tile * KEYS, kw = kg + block * 32, key = kw + (lane & 31);
 
     // Rows of this walk: positions p0 .. p1.
-    const int last = min(kg + kKeysPerGroup, s.nk) - 1;
+    const int last = min(kg + KEYS, s.nk) - 1;
     int p0 = kg, p1 = (int)min((int64_t)last + a.window - 1, (int64_t)s.nk - 1);
     if (chunk >= 0) {
-        p0 = (int)min((int64_t)kg + kKeysPerGroup - 1 + a.window + (int64_t)chunk * a.chunk_len, (int64_t)s.nk);
+        p0 = (int)min((int64_t)kg + KEYS - 1 + a.window + (int64_t)chunk * a.chunk_len, (int64_t)s.nk);
         p1 = (int)min((int64_t)p0 + a.chunk_len - 1, (int64_t)s.nk - 1);
     }
     const int i0 = max(0, p0 - s.off), i1 = p1 - s.off;
@@ -183,7 +186,7 @@ __global__ __launch_bounds__(256, 2) void attn_dkv_kernel(const AttnParams a)
     const int r_end = last < kg || i1 < i0 ? 0 : (i1 + 1) * a.G;
     const int n = r_end > rt0 ? (r_end - rt0 + kRowTile - 1) / kRowTile : 0;
 
-    RowStage<LP> stage(a, b, hk, bh, rt0, r_end);
+    RowStage<LP, NW> stage(a, b, hk, bh, rt0, r_end);
     if (n > 0) stage.copy(lds);
     const Tensor& mine = second ? a.v : a.k;
     u32x4_t kv[KS];
@@ -213,10 +216,11 @@ __global__ __launch_bounds__(256, 2) void attn_dkv_kernel(const AttnParams a)
         const int pa = s.off + (int)a.by_group.div(rt), pb = s.off + (int)a.by_group.div(rb);
         // Nothing here is seen by these keys.
         if (pb < kw || (pa - (kw + 31) >= a.window && kw >= a.sinks)) continue;
-        const u32 rows = buf + (second ? TILE : 0), cols = buf + (second ? 0 : TILE);
+        const RowsOf<LP> rows(buf + (second ? TILE : 0), lane & 31);
+        const ColsOf<LP> cols(buf + (second ? 0 : TILE));
         floatx16_t x = {};
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) x = mfma<BF>(read_rows<LP>(rows, lane & 31, ks * 16 + h * 8), kv[ks], x);
+        for (int ks = 0; ks < KS; ++ks) x = mfma<BF>(rows.get(ks), kv[ks], x);
         read_ahead<KS, 1, 4>();
         const u32 stat = buf + 2 * TILE + (second ? 128 : 0) + 16 * h;
         floatx4_t st[4];
@@ -265,7 +269,7 @@ __global__ __launch_bounds__(256, 2) void attn_dkv_kernel(const AttnParams a)
 #pragma unroll
         for (int s2 = 0; s2 < 2; ++s2)
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) acc[mt] = mfma<BF>(read_cols<LP>(cols, s2 * 16, mt * 32), op[s2], acc[mt]);
+            for (int mt = 0; mt < MT; ++mt) acc[mt] = mfma<BF>(cols.get(s2 * 16, mt), op[s2], acc[mt]);
         read_ahead<2 * MT, 2, MT>();
     }
 
@@ -335,9 +339,14 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnParams a)
     const int pw_lo = s.off + (int)a.by_group.div(rw), pw_hi = s.off + min((int)a.by_group.div(rw + 31), s.nq - 1);
     const int p = s.off + (int)a.by_group.div(r);
 
-    KeyStage<LP, NW> stage(a, kt, b, hk);
+    KeyStage<LP, NW, false> stage(a, kt, b, hk);
     stage.clear(lds, 4 * TILE, a.D);
-    if (kt.n > 0) stage.copy(kt.at(0), lds);
+    const typename KeyStage<LP, NW, false>::Pages none{};
+    const auto copy = [&](int t, u32 at) {
+        stage.copy(a.k, t, none, at);
+        stage.copy(a.v, t, none, at + TILE);
+    };
+    if (kt.n > 0) copy(kt.at(0), lds);
 
     u32x4_t q[KS], dout[KS];
 #pragma unroll
@@ -358,27 +367,26 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnParams a)
     for (int it = 0; it < kt.n; ++it) {
         const u32 buf = lds + (it & 1) * (2 * TILE), nbuf = lds + ((it + 1) & 1) * (2 * TILE);
         sync_all();
-        if (it + 1 < kt.n) stage.copy(kt.at(it + 1), nbuf);
+        if (it + 1 < kt.n) copy(kt.at(it + 1), nbuf);
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
             const int k0 = kt.at(it) * kKeyTile + kb * 32;
             if (rw >= r_end || k0 > pw_hi || (k0 + 31 <= pw_lo - a.window && k0 >= a.sinks)) continue;
+            const RowsOf<LP> kr(buf, lane & 31), vr(buf + TILE, lane & 31);
+            const ColsOf<LP> kc(buf);
             floatx16_t sc = {}, dp = {};
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-                sc = mfma<BF>(read_rows<LP>(buf, kb * 32 + (lane & 31), ks * 16 + h * 8), q[ks], sc);
-                dp = mfma<BF>(read_rows<LP>(buf + TILE, kb * 32 + (lane & 31), ks * 16 + h * 8), dout[ks], dp);
+                sc = mfma<BF>(kr.get(ks, kb), q[ks], sc);
+                dp = mfma<BF>(vr.get(ks, kb), dout[ks], dp);
             }
             read_ahead<2 * KS, 1, 4>();
 #pragma unroll
             for (int i = 0; i < 16; ++i) sc[i] = fmaf(sc[i], c, -l2);
             if (k0 + 31 > pw_lo || k0 <= pw_hi - a.window) {
+                const Mask see(p, k0 + 4 * h, a);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int j = k0 + 8 * (i / 4) + 4 * h + i % 4;
-                    const bool seen = j <= p && (j > p - a.window || j < a.sinks);
-                    sc[i] = seen ? sc[i] : -INFINITY;
-                }
+                for (int i = 0; i < 16; ++i) sc[i] = see(8 * (i / 4) + i % 4) ? sc[i] : -INFINITY;
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i) dp[i] -= delta;
@@ -400,7 +408,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnParams a)
             for (int s2 = 0; s2 < 2; ++s2)
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
-                    dq[mt] = mfma<BF>(read_cols<LP>(buf, kb * 32 + s2 * 16, mt * 32), ds[s2], dq[mt]);
+                    dq[mt] = mfma<BF>(kc.get(kb * 32 + s2 * 16, mt), ds[s2], dq[mt]);
             read_ahead<2 * MT, 2, MT>();
         }
     }
@@ -421,7 +429,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnParams a)
 }
 
 template <bool BF>
-int run(AttnParams a, hipStream_t st)
+int run(AttnParams a, int group_keys, hipStream_t st)
 {
     const int64_t heads = (int64_t)a.B * a.Hkv;
     attn_stat_kernel<BF><<<(unsigned)((heads * a.stat_rows + 15) / 16), 256, 0, st>>>(a);
@@ -430,7 +438,9 @@ int run(AttnParams a, hipStream_t st)
     a.tiles = ceil_div(a.rows, 128);
     rc = with_head(a.D, [&](auto DP) {
         const int items = a.key_tiles + a.sink_tiles * a.chunks;
-        if (items) attn_dkv_kernel<BF, DP.value><<<(unsigned)(heads * items), 256, 0, st>>>(a);
+        const unsigned grid = (unsigned)(heads * items);
+        if (items && group_keys == 128) attn_dkv_kernel<BF, DP.value, 8><<<grid, 512, 0, st>>>(a);
+        else if (items) attn_dkv_kernel<BF, DP.value, 4><<<grid, 256, 0, st>>>(a);
         if (a.tiles) attn_dq_kernel<BF, DP.value><<<(unsigned)(heads * a.tiles), 256, 0, st>>>(a);
         return launch_status();
     });
@@ -443,6 +453,7 @@ int run(AttnParams a, hipStream_t st)
 
 }  // namespace
 
+// Groups of 128 keys where they fill the card's 256 CUs, else of 64.
 // Sink keys' rows past the window are cut into chunks of about 512 flattened
 // rows, so that they are spread over the card, as long as that makes no more
 // than 256 workgroups; no chunk walks further than the window's own walk
@@ -451,13 +462,14 @@ AttnBwdPlan attn_bwd_plan(const AttnParams& a)
 {
     AttnBwdPlan p{};
     p.stat_rows = ceil_div(a.rows, kRowTile) * kRowTile + kRowTile;
-    p.key_tiles = ceil_div(a.Lk, kKeysPerGroup);
+    p.group_keys = (int64_t)a.B * a.Hkv * ceil_div(a.Lk, 128) >= 256 ? 128 : 64;
+    p.key_tiles = ceil_div(a.Lk, p.group_keys);
     // Positions past the first key tile's window, if any key there is a sink.
-    const int64_t past = (int64_t)a.Lk - (kKeysPerGroup - 1) - a.window;
+    const int64_t past = (int64_t)a.Lk - (p.group_keys - 1) - a.window;
     const int64_t heads = (int64_t)a.B * a.Hkv;
     if (a.sinks > 0 && past > 0) {
-        p.sink_tiles = ceil_div(a.sinks, kKeysPerGroup);
-        const int64_t fine = ceil_div(512, a.G), own = (int64_t)a.window + kKeysPerGroup;
+        p.sink_tiles = ceil_div(a.sinks, p.group_keys);
+        const int64_t fine = ceil_div(512, a.G), own = (int64_t)a.window + p.group_keys;
         int64_t chunks = std::min((past + fine - 1) / fine, std::max<int64_t>(1, 256 / (heads * p.sink_tiles)));
         chunks = std::max(chunks, (past + own - 1) / own);
         chunks = std::max<int64_t>(1, std::min(chunks, (int64_t(1) << 27) / (heads * a.sinks * a.D)));
@@ -481,7 +493,7 @@ int launch_attn_bwd(AttnParams a, const AttnBwdPlan& p, void* ws, bool bf, hipSt
     a.sink_tiles = p.sink_tiles;
     a.chunks = p.chunks;
     a.chunk_len = p.chunk_len;
-    return bf ? run<true>(a, st) : run<false>(a, st);
+    return bf ? run<true>(a, p.group_keys, st) : run<false>(a, p.group_keys, st);
 }
 
 }  // namespace seq

@@ -24,7 +24,7 @@ namespace im2win {
 namespace seq {
 namespace {
 
-template <bool BF, int DP, int NW>
+template <bool BF, int DP, int NW, bool PAGED>
 __global__ __launch_bounds__(NW * 64, NW > 2 ? 2 : 1) void attn_fwd_kernel(const AttnParams a)
 {
     constexpr int LP = row_pitch(DP), KS = DP / 16, MT = DP / 32, TILE = kKeyTile * LP * 2;
@@ -48,12 +48,14 @@ __global__ __launch_bounds__(NW * 64, NW > 2 ? 2 : 1) void attn_fwd_kernel(const
     const int pw_lo = s.off + (int)a.by_group.div(rw), pw_hi = s.off + min((int)a.by_group.div(rw + 31), s.nq - 1);
     const int p = s.off + (int)a.by_group.div(r);
 
-    KeyStage<LP, NW> stage(a, kt, b, hk);
+    const KeyStage<LP, NW, PAGED> stage(a, kt, b, hk);
+    typename KeyStage<LP, NW, PAGED>::Pages ahead{};  // pages of the next tile
     stage.clear(lds, 4 * TILE, a.D);
     if (it0 < it1) {
-        stage.look_up(kt.at(it0));
-        stage.copy(kt.at(it0), lds);
-        if (it0 + 1 < it1) stage.look_up(kt.at(it0 + 1));
+        stage.look_up(kt.at(it0), ahead);
+        stage.copy(a.k, kt.at(it0), ahead, lds);
+        stage.copy(a.v, kt.at(it0), ahead, lds + TILE);
+        if (it0 + 1 < it1) stage.look_up(kt.at(it0 + 1), ahead);
     }
 
     // A negative scale flips the rows' sign (exact), so that the largest
@@ -76,28 +78,28 @@ __global__ __launch_bounds__(NW * 64, NW > 2 ? 2 : 1) void attn_fwd_kernel(const
         const u32 buf = lds + ((it - it0) & 1) * (2 * TILE), nbuf = lds + ((it - it0 + 1) & 1) * (2 * TILE);
         sync_all();
         if (it + 1 < it1) {
-            stage.copy(kt.at(it + 1), nbuf);
-            if (it + 2 < it1) stage.look_up(kt.at(it + 2));
+            stage.copy(a.k, kt.at(it + 1), ahead, nbuf);
+            stage.copy(a.v, kt.at(it + 1), ahead, nbuf + TILE);
+            if (it + 2 < it1) stage.look_up(kt.at(it + 2), ahead);
         }
         const int k0 = kt.at(it) * kKeyTile;
         if (rw >= r_end || k0 > pw_hi || (k0 + kKeyTile - 1 <= pw_lo - a.window && k0 >= a.sinks)) continue;
 
+        const RowsOf<LP> kr(buf, lane & 31);
+        const ColsOf<LP> vc(buf + TILE);
         floatx16_t sc[2] = {};
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb)
-                sc[kb] = mfma<BF>(read_rows<LP>(buf, kb * 32 + (lane & 31), ks * 16 + h * 8), q[ks], sc[kb]);
+                sc[kb] = mfma<BF>(kr.get(ks, kb), q[ks], sc[kb]);
         read_ahead<2 * KS, 1, 6>();
         if (k0 + kKeyTile - 1 > pw_lo || k0 <= pw_hi - a.window) {
+            const Mask see(p, k0 + 4 * h, a);
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int j = k0 + kb * 32 + 8 * (i / 4) + 4 * h + i % 4;
-                    const bool seen = j <= p && (j > p - a.window || j < a.sinks);
-                    sc[kb][i] = seen ? sc[kb][i] : -INFINITY;
-                }
+                for (int i = 0; i < 16; ++i) sc[kb][i] = see(kb * 32 + 8 * (i / 4) + i % 4) ? sc[kb][i] : -INFINITY;
         }
         float top = sc[0][0];
 #pragma unroll
@@ -131,7 +133,7 @@ __global__ __launch_bounds__(NW * 64, NW > 2 ? 2 : 1) void attn_fwd_kernel(const
         for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
-                o[mt] = mfma<BF>(read_cols<LP>(buf + TILE, ks * 16, mt * 32), pr[ks], o[mt]);
+                o[mt] = mfma<BF>(vc.get(ks * 16, mt), pr[ks], o[mt]);
         read_ahead<4 * MT, 2, 4>();
     }
 
@@ -213,7 +215,8 @@ int run(const AttnParams& a, hipStream_t st)
 {
     const unsigned grid = (unsigned)((int64_t)a.B * a.Hkv * a.tiles * a.nsplit);
     return with_head(a.D, [&](auto DP) {
-        attn_fwd_kernel<BF, DP.value, NW><<<grid, NW * 64, 0, st>>>(a);
+        if (a.table) attn_fwd_kernel<BF, DP.value, NW, true><<<grid, NW * 64, 0, st>>>(a);
+        else attn_fwd_kernel<BF, DP.value, NW, false><<<grid, NW * 64, 0, st>>>(a);
         return launch_status();
     });
 }

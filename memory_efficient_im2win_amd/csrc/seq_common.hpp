@@ -67,34 +67,19 @@ __device__ __forceinline__ floatx16_t mfma(u32x4_t a, u32x4_t b, floatx16_t c)
 }
 
 // 16 bytes per lane from p into LDS at byte lds + 16 * lane (lds the same for
-// the wave; M0 restored). Counts in vmcnt.
+// the wave). Counts in vmcnt. Nothing else in these kernels uses M0.
 __device__ __forceinline__ void dma16(const void* p, u32 lds)
 {
-    u32 save;
-    asm volatile(
-        "s_mov_b32 %0, m0\n\t"
-        "s_mov_b32 m0, %1\n\t"
-        "s_nop 0\n\t"
-        "global_load_lds_dwordx4 %2, off\n\t"
-        "s_mov_b32 m0, %0"
-        : "=&s"(save)
-        : "s"(uniform(lds)), "v"(p)
-        : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(uniform(lds)), "v"(p)
+                 : "memory");
 }
 
 // The same from a wave-uniform base and a lane offset.
 __device__ __forceinline__ void dma16(const void* base, u32 offset, u32 lds)
 {
-    u32 save;
-    asm volatile(
-        "s_mov_b32 %0, m0\n\t"
-        "s_mov_b32 m0, %1\n\t"
-        "s_nop 0\n\t"
-        "global_load_lds_dwordx4 %2, %3\n\t"
-        "s_mov_b32 m0, %0"
-        : "=&s"(save)
-        : "s"(uniform(lds)), "v"(offset), "s"(base)
-        : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(uniform(lds)), "v"(offset),
+                 "s"(base)
+                 : "memory");
 }
 
 // Waits for this wave's loads, visibly to the compiler: a load that it still
@@ -133,13 +118,6 @@ __device__ __forceinline__ u32 swz(u32 row)
     else return ((row & 2) << 1) | ((row >> 2) & 3);
 }
 
-// Byte offset of element (row, col) in a tile.
-template <int LP>
-__device__ __forceinline__ u32 tile_at(u32 row, u32 col)
-{
-    return row * (LP * 2) + (((col >> 3) ^ swz<LP>(row)) << 4) + (col & 7) * 2;
-}
-
 typedef __attribute__((address_space(3))) unsigned char lds_byte;
 
 __device__ __forceinline__ u32x4_t lds_read16(u32 at)
@@ -152,37 +130,56 @@ __device__ __forceinline__ void lds_write16(u32 at, u32x4_t v)
     *(__attribute__((address_space(3))) u32x4_t*)(uintptr_t)at = v;
 }
 
-// Depths d0 + 8h .. + 7 of row `row`: an operand whose rows are tokens.
-template <int LP>
-__device__ __forceinline__ u32x4_t read_rows(u32 tile, u32 row, u32 col)
-{
-    return lds_read16(tile + tile_at<LP>(row, col));
-}
+// Reading operands. A reader holds one address; every other one of a tile is
+// that address XOR a constant (tiles are aligned to their rows, and a chunk's
+// position is an XOR) plus a constant, so no other addresses are kept.
 
-// Transposed read: the operand whose row is dimension c0 + (lane % 32) and
-// whose depths are the tokens r0 + 4h + {0..3} and r0 + 8 + 4h + {0..3}.
+// Rows are tokens: row `row` of the tile, depths 16 * ks + 8 * h .. + 7.
+template <int LP>
+struct RowsOf {
+    u32 at;
+    __device__ __forceinline__ RowsOf(u32 tile, u32 row)
+        : at(tile + row * (LP * 2) + ((((threadIdx.x & 63) >> 5) ^ swz<LP>(row)) << 4))
+    {
+    }
+    // The same row of the block of 32 rows `block` further on.
+    __device__ __forceinline__ u32x4_t get(int ks, int block = 0) const
+    {
+        return lds_read16((at ^ (u32)(ks * 32)) + block * (32 * LP * 2));
+    }
+};
+
+// Transposed: rows are the dimensions 32 * mt + lane % 32, depths the tokens
+// r0 + 4h + {0..3} and r0 + 8 + 4h + {0..3}, r0 a multiple of 16.
 // ds_read_b64_tr_b16 turns, for each 16 lanes, 4 rows of 16 elements (lane i
 // points at 4 elements: row i / 4, elements 4 * (i % 4)) into 16 columns of 4.
-// PI: dimension of operand row 16g + 4a + b is 16g' + ... with the 4-groups
-// ordered so that result rows (see above) read 8 dimensions in order.
+// PI: dimensions in another order inside the 32, so that result registers
+// 8s .. 8s+7 of half h (see above) are the dimensions 16s + 8h .. + 7.
 template <int LP, bool PI = false>
-__device__ __forceinline__ u32x4_t read_cols(u32 tile, u32 r0, u32 c0)
-{
-    const u32 lane = threadIdx.x & 63;
-    const u32 h = lane >> 5, i = lane & 15, half16 = (lane >> 4) & 1;
-    const u32 row = r0 + 4 * h + (i >> 2);
-    u32 g4 = half16 * 4 + (i & 3);  // 4-group of dimensions, 0..7 in the block of 32
-    if constexpr (PI) g4 = (g4 & 4) | ((g4 & 1) << 1) | ((g4 >> 1) & 1);
-    const u32 col = c0 + 4 * g4;
-    typedef __attribute__((address_space(3))) short4_t* ptr;
-    const short4_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ptr)(uintptr_t)(tile + tile_at<LP>(row, col)));
-    const short4_t b =
-        __builtin_amdgcn_ds_read_tr16_b64_v4i16((ptr)(uintptr_t)(tile + tile_at<LP>(row + 8, col)));
-    u32x4_t r;
-    const u32x2_t ua = __builtin_bit_cast(u32x2_t, a), ub = __builtin_bit_cast(u32x2_t, b);
-    r.x = ua.x, r.y = ua.y, r.z = ub.x, r.w = ub.y;
-    return r;
-}
+struct ColsOf {
+    u32 at;
+    __device__ __forceinline__ ColsOf(u32 tile, int first_mt = 0)
+    {
+        const u32 lane = threadIdx.x & 63, i = lane & 15;
+        const u32 row = 4 * (lane >> 5) + (i >> 2);
+        u32 g4 = ((lane >> 4) & 1) * 4 + (i & 3);  // 4-group of dimensions, 0..7 in the block of 32
+        if constexpr (PI) g4 = (g4 & 4) | ((g4 & 1) << 1) | ((g4 >> 1) & 1);
+        at = tile + row * (LP * 2) + ((((u32)first_mt * 4 + (g4 >> 1)) ^ swz<LP>(row)) << 4) + (g4 & 1) * 8;
+    }
+    __device__ __forceinline__ u32x4_t get(int r0, int mt) const
+    {
+        // 8 rows on, the row's swizzle has another bit 1.
+        const u32 x = at ^ (u32)(mt * 64), y = (x ^ 32u) + 8 * LP * 2;
+        typedef __attribute__((address_space(3))) short4_t* ptr;
+        const u32x2_t a = __builtin_bit_cast(
+            u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((ptr)(uintptr_t)(x + r0 * (LP * 2))));
+        const u32x2_t b = __builtin_bit_cast(
+            u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((ptr)(uintptr_t)(y + r0 * (LP * 2))));
+        u32x4_t r;
+        r.x = a.x, r.y = a.y, r.z = b.x, r.w = b.y;
+        return r;
+    }
+};
 
 // Sum and maximum over a lane and the lane 32 away.
 __device__ __forceinline__ float half_sum(float v)

@@ -33,8 +33,6 @@ struct AttnParams {
     int pages, window, sinks;
     float scale;
     FastDiv by_group, by_page;
-    bool short_rows;  // 32-bit offsets reach across a tile's keys
-    bool same_kv;     // k and v have the same strides
     // Forward: key tiles split over nsplit workgroups, partial results in ws.
     int nsplit, tiles;
     float* part;
@@ -54,7 +52,7 @@ AttnPlan attn_plan(const AttnParams& a);
 int launch_attn_fwd(AttnParams a, const AttnPlan& plan, bool bf, hipStream_t st);
 
 struct AttnBwdPlan {
-    int stat_rows, key_tiles, sink_tiles, chunks, chunk_len;
+    int stat_rows, group_keys, key_tiles, sink_tiles, chunks, chunk_len;
     size_t stat_bytes, ws_bytes;
 };
 AttnBwdPlan attn_bwd_plan(const AttnParams& a);

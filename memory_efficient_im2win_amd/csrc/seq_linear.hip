@@ -154,16 +154,19 @@ __global__ __launch_bounds__(DVP * 2, 2) void linear_kernel(const LinParams a)
         if (t + kChunk < t_live) stage(t + kChunk, lds + ((it + 1) & 1) * BUF);
         if (tokens < kChunk) set_to_end(tokens);
 
+        const RowsOf<LK> kr(kt, col), qr(qt, col);
+        const ColsOf<LV> vc(vt, wave);
+        const ColsOf<LK, true> kc(kt);
         u32x4_t v[2];
 #pragma unroll
-        for (int s = 0; s < 2; ++s) v[s] = read_cols<LV>(vt, s * 16, wave * 32);
+        for (int s = 0; s < 2; ++s) v[s] = vc.get(s * 16, 0);
         if (OUT) {
             u32x4_t q[KS];
             floatx16_t sc = {}, o = {};
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-                q[ks] = read_rows<LK>(qt, col, ks * 16 + h * 8);
-                sc = mfma<BF>(read_rows<LK>(kt, col, ks * 16 + h * 8), q[ks], sc);
+                q[ks] = qr.get(ks);
+                sc = mfma<BF>(kr.get(ks), q[ks], sc);
             }
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
@@ -204,7 +207,7 @@ __global__ __launch_bounds__(DVP * 2, 2) void linear_kernel(const LinParams a)
             split_parts<BF, PARTS>(v[s], to_end[s], w);
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-                const u32x4_t k = read_cols<LK, true>(kt, s * 16, mt * 32);
+                const u32x4_t k = kc.get(s * 16, mt);
 #pragma unroll
                 for (int p = 0; p < PARTS; ++p) S[mt] = mfma<BF>(k, w[p], S[mt]);
             }

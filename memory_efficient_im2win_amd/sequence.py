@@ -64,9 +64,9 @@ def _tensor(t, name, like, shape):
     # The stride of an extent of one means nothing.
     sb, sl, sh = sb if B > 1 else 0, sl if L > 1 else 0, sh if H > 1 else 0
     p = t.data_ptr()
-    if sd != 1 or (sb | sl | sh) & 7 or p & 15:
+    if sd != 1 or (sb | sl | sh) & 7 or p & 15 or sl >= 1 << 24:
         raise ValueError(f"{name} needs an innermost stride of 1, other strides that are multiples of 8 elements "
-                         "and a 16-byte aligned start")
+                         "(from token to token below 2**24) and a 16-byte aligned start")
     return p, sb, sl, sh
 
 

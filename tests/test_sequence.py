@@ -88,7 +88,8 @@ def _linear(q=T, k=T, v=T, out=T, decay=FAKE, state_in=0, state_out=0, lens=0, d
                                  *dout, *dq, *dk, *dv, dstate_out, dstate_in)
 
 
-BAD_TENSORS = [(0, 64, 64, 64), (FAKE + 8, 64, 64, 64), (FAKE, 60, 64, 64), (FAKE, 64, 4, 64), (FAKE, 64, 64, -64)]
+BAD_TENSORS = [(0, 64, 64, 64), (FAKE + 8, 64, 64, 64), (FAKE, 60, 64, 64), (FAKE, 64, 4, 64), (FAKE, 64, 64, -64),
+               (FAKE, 64, 1 << 24, 64)]
 BAD_ATTENTION = ([dict(dtype=2), dict(dtype=-1), dict(B=-1), dict(Lq=-1), dict(Lk=-1), dict(Hq=3, Hkv=2), dict(Hkv=0),
                   dict(Hq=0), dict(D=0), dict(D=12), dict(D=136), dict(window=0), dict(sinks=-1),
                   dict(scale=float("nan")), dict(scale=float("inf")), dict(Lq=1 << 30), dict(Lk=(1 << 30) + 1),
