@@ -302,20 +302,28 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_dkv_kernel(const AttnParams a
         }
 }
 
-// Sums a sink key's parts in order. A quarter of D lanes hold a key.
+// Sums a sink key's parts. 32 lanes hold a row of dk or dv, 4 dimensions
+// each; 8 groups of them take every 8th part, and join in a fixed order.
 template <bool BF>
-__global__ __launch_bounds__(256) void attn_sink_join_kernel(const AttnParams a, int lanes)
+__global__ __launch_bounds__(256) void attn_sink_join_kernel(const AttnParams a)
 {
-    const int per = 256 / lanes, sub = threadIdx.x / lanes, d = threadIdx.x % lanes * 4;
-    const int64_t at = (int64_t)blockIdx.x * per + sub;
-    const int which = (int)(at & 1), key = (int)((at >> 1) % a.sinks);
-    const int64_t bh = (at >> 1) / a.sinks;
-    if (sub >= per || bh >= (int64_t)a.B * a.Hkv || d >= a.D) return;
-    const int b = (int)(bh / a.Hkv), hk = (int)(bh % a.Hkv);
+    __shared__ floatx4_t part[8][32];
+    const int group = threadIdx.x / 32, lane = threadIdx.x & 31, d = lane * 4;
+    const int which = blockIdx.x & 1, key = (blockIdx.x >> 1) % a.sinks;
+    const int64_t bh = (blockIdx.x >> 1) / a.sinks;
     floatx4_t x = {0, 0, 0, 0};
-    for (int c = 0; c <= a.chunks; ++c)
-        x += *(const floatx4_t*)(a.part + (((bh * (a.chunks + 1) + c) * 2 + which) * a.sinks + key) * a.D + d);
+    if (d < a.D) {
+#pragma unroll 4
+        for (int c = group; c <= a.chunks; c += 8)
+            x += *(const floatx4_t*)(a.part + (((bh * (a.chunks + 1) + c) * 2 + which) * a.sinks + key) * a.D + d);
+    }
+    part[group][lane] = x;
+    __syncthreads();
+    if (group || d >= a.D) return;
+#pragma unroll
+    for (int j = 1; j < 8; ++j) x += part[j][lane];
     if (!which) x *= a.scale;
+    const int b = (int)(bh / a.Hkv), hk = (int)(bh % a.Hkv);
     const Tensor& t = which ? a.dv : a.dk;
     const u32x2_t w = {pack2<BF>(x[0], x[1]), pack2<BF>(x[2], x[3])};
     *(u32x2_t*)(t.p + b * t.sb + key * t.sl + hk * t.sh + d * 2) = w;
@@ -445,9 +453,7 @@ int run(AttnParams a, int group_keys, hipStream_t st)
         return launch_status();
     });
     if (rc != 0 || a.sink_tiles == 0) return rc;
-    const int lanes = a.D / 4, per = 256 / lanes;
-    const int64_t all = heads * a.sinks * 2;
-    attn_sink_join_kernel<BF><<<(unsigned)((all + per - 1) / per), 256, 0, st>>>(a, lanes);
+    attn_sink_join_kernel<BF><<<(unsigned)(heads * a.sinks * 2), 256, 0, st>>>(a);
     return launch_status();
 }
 

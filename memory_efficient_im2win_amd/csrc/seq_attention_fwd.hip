@@ -176,34 +176,60 @@ __global__ __launch_bounds__(NW * 64, NW > 2 ? 2 : 1) void attn_fwd_kernel(const
 }
 
 // Joins the splits of a row: out = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s.
-// D / 4 lanes hold a row, 4 dimensions each.
-template <bool BF>
-__global__ __launch_bounds__(256) void attn_join_kernel(const AttnParams a, int lanes)
+// 32 lanes hold a row, 4 dimensions each; P groups of them take every P-th
+// split, side by side, and join through LDS in a fixed order.
+template <bool BF, int P>
+__global__ __launch_bounds__(256) void attn_join_kernel(const AttnParams a)
 {
-    const int per = 256 / lanes, sub = threadIdx.x / lanes, d = threadIdx.x % lanes * 4;
-    const int64_t row = (int64_t)blockIdx.x * per + sub, all = (int64_t)a.B * a.Hkv * a.rows;
-    if (sub >= per || row >= all || d >= a.D) return;
-    const int bh = (int)(row / a.rows), r = (int)(row % a.rows), b = bh / a.Hkv, hk = bh % a.Hkv;
-    const int i = a.by_group.div(r), g = r - i * a.G;
+    __shared__ float part_m[8], part_l[8];
+    __shared__ floatx4_t part_o[8][32];
+    const int group = threadIdx.x / 32, lane = threadIdx.x & 31, d = lane * 4;
+    const int64_t row = (int64_t)blockIdx.x * (8 / P) + group / P, all = (int64_t)a.B * a.Hkv * a.rows;
+    const int bh = (int)min(row / a.rows, (int64_t)a.B * a.Hkv - 1), r = (int)(row % a.rows);
+    const int b = bh / a.Hkv, hk = bh % a.Hkv, i = a.by_group.div(r), g = r - i * a.G;
     const Span s(a, b);
+    const bool on = row < all && i < s.nq;
     const float* part = a.part + row * (a.D + 2);
     const int64_t step = all * (a.D + 2);
     float m = -INFINITY, l = 0;
     floatx4_t o = {0, 0, 0, 0};
-    if (i < s.nq) {
-        for (int j = 0; j < a.nsplit; ++j) m = fmaxf(m, part[j * step]);
-        const float mu = m == -INFINITY ? 0.0f : m;
-        for (int j = 0; j < a.nsplit; ++j) {
+    const auto add = [&](float m1, float l1, floatx4_t o1) {
+        const float top = fmaxf(m, m1), f = m == top ? 1.0f : __builtin_amdgcn_exp2f(m - top);
+        const float f1 = m1 == top ? 1.0f : __builtin_amdgcn_exp2f(m1 - top);
+        m = top;
+        l = l * f + l1 * f1;
+        o = o * f + o1 * f1;
+    };
+    if (on) {
+#pragma unroll 4
+        for (int j = group % P; j < a.nsplit; j += P) {
             const float* x = part + j * step;
-            const floatx2_t lo = *(const floatx2_t*)(x + 2 + d), hi = *(const floatx2_t*)(x + 4 + d);
-            const float f = __builtin_amdgcn_exp2f(x[0] - mu);
-            l += f * x[1];
-            o[0] += f * lo[0], o[1] += f * lo[1], o[2] += f * hi[0], o[3] += f * hi[1];
+            const floatx2_t ml = *(const floatx2_t*)x;
+            floatx2_t lo = {0, 0}, hi = {0, 0};
+            if (d < a.D) {
+                lo = *(const floatx2_t*)(x + 2 + d);
+                hi = *(const floatx2_t*)(x + 4 + d);
+            }
+            const floatx4_t o1 = {lo[0], lo[1], hi[0], hi[1]};
+            if (ml[0] != -INFINITY) add(ml[0], ml[1], o1);
         }
     }
+    if (P > 1) {
+        if (lane == 0) {
+            part_m[group] = m;
+            part_l[group] = l;
+        }
+        part_o[group][lane] = o;
+        __syncthreads();
+        if (group % P) return;
+#pragma unroll
+        for (int j = 1; j < P; ++j)
+            if (part_m[group + j] != -INFINITY) add(part_m[group + j], part_l[group + j], part_o[group + j][lane]);
+    }
+    if (row >= all || d >= a.D) return;
     const float inv = l != 0 ? 1.0f / l : 0.0f;
     unsigned char* out = a.out.p + b * a.out.sb + i * a.out.sl + (int64_t)(hk * a.G + g) * a.out.sh;
-    u32x2_t w = {pack2<BF>(o[0] * inv, o[1] * inv), pack2<BF>(o[2] * inv, o[3] * inv)};
+    const u32x2_t w = {pack2<BF>(o[0] * inv, o[1] * inv), pack2<BF>(o[2] * inv, o[3] * inv)};
     *(u32x2_t*)(out + d * 2) = w;
     if (a.lse && d == 0)
         a.lse[((int64_t)b * a.Hq + hk * a.G + g) * a.Lq + i] =
@@ -223,9 +249,9 @@ int run(const AttnParams& a, hipStream_t st)
 
 }  // namespace
 
-// Tiles of 128 rows where they fill the card's 256 CUs, else of 32; where
-// even those leave it idle, the keys are split until 512 workgroups are
-// there or a workgroup is down to two key tiles.
+// Tiles of 128 rows where they fill the card's 256 CUs, else of 32; where even
+// those leave it idle, the keys are split until 512 workgroups are there or a
+// workgroup is down to one key tile.
 AttnPlan attn_plan(const AttnParams& a)
 {
     AttnPlan p{};
@@ -234,8 +260,8 @@ AttnPlan attn_plan(const AttnParams& a)
     p.tiles = ceil_div(a.rows, p.waves * 32);
     const int64_t groups = heads * p.tiles;
     const int64_t keys = std::min<int64_t>((int64_t)a.window + p.waves * 32 / a.G, a.Lk) + std::min(a.sinks, a.Lk);
-    const int64_t most = std::max<int64_t>(1, keys / (2 * kKeyTile));
-    p.nsplit = groups >= 512 ? 1 : (int)std::min<int64_t>(most, (512 + groups - 1) / groups);
+    const int64_t most = std::max<int64_t>(1, (keys + kKeyTile - 1) / kKeyTile);
+    p.nsplit = p.waves == 4 ? 1 : (int)std::min<int64_t>(most, (512 + groups - 1) / groups);
     p.ws_bytes = p.nsplit > 1 ? (size_t)p.nsplit * heads * a.rows * (a.D + 2) * 4 : 0;
     return p;
 }
@@ -248,11 +274,15 @@ int launch_attn_fwd(AttnParams a, const AttnPlan& plan, bool bf, hipStream_t st)
     if (plan.waves == 4) rc = bf ? run<true, 4>(a, st) : run<false, 4>(a, st);
     else rc = bf ? run<true, 1>(a, st) : run<false, 1>(a, st);
     if (rc != 0 || a.nsplit == 1) return rc;
-    const int lanes = a.D / 4, per = 256 / lanes;
     const int64_t all = (int64_t)a.B * a.Hkv * a.rows;
-    const unsigned grid = (unsigned)((all + per - 1) / per);
-    if (bf) attn_join_kernel<true><<<grid, 256, 0, st>>>(a, lanes);
-    else attn_join_kernel<false><<<grid, 256, 0, st>>>(a, lanes);
+    if (a.nsplit < 8) {
+        const unsigned grid = (unsigned)((all + 7) / 8);
+        if (bf) attn_join_kernel<true, 1><<<grid, 256, 0, st>>>(a);
+        else attn_join_kernel<false, 1><<<grid, 256, 0, st>>>(a);
+    } else {
+        if (bf) attn_join_kernel<true, 8><<<(unsigned)all, 256, 0, st>>>(a);
+        else attn_join_kernel<false, 8><<<(unsigned)all, 256, 0, st>>>(a);
+    }
     return launch_status();
 }
 
