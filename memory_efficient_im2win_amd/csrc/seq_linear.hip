@@ -37,23 +37,32 @@ enum Mode { kStates, kOutputs, kWhole };
 // Position of token t of the walk; absent tokens (t >= n) keep their place.
 __device__ __forceinline__ int walk(int t, int n, bool reverse) { return reverse && t < n ? n - 1 - t : t; }
 
-// Copies 32 tokens of x from walk position t0 into the LDS tile.
+// Copies 32 tokens of a tensor (x: its first token of the head) from walk
+// position t0 into the LDS tile. Chunks past the head size are not written:
+// they are zeroed once.
 template <int LP, int NW>
-__device__ __forceinline__ void stage_tokens(const Tensor& x, int b, int hd, int d, int t0, int n, bool reverse,
+__device__ __forceinline__ void stage_tokens(const unsigned char* x, int64_t sl, int d, int t0, int n, bool reverse,
                                              u32 lds)
 {
     constexpr int CH = LP / 8, RPI = 64 / CH, N = kChunk / RPI;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const bool whole = t0 + kChunk <= n;
+    // The tile's token with the lowest address, and the lane's row from there.
+    const unsigned char* first = x + (reverse ? n - t0 - kChunk : t0) * sl;
 #pragma unroll
     for (int j = 0; j < (N + NW - 1) / NW; ++j) {
         const int part = j * NW + wave;
         if (N % NW != 0 && part >= N) break;
         const u32 row = part * RPI + lane / CH;
         const u32 c = (lane % CH) ^ swz<LP>(row);
-        const int t = t0 + (int)row;
-        const unsigned char* p = (const unsigned char*)kAbsent.zero;
-        if (t < n && (int)c * 8 < d) p = x.p + b * x.sb + walk(t, n, reverse) * x.sl + hd * x.sh + c * 16;
-        dma16(p, lds + part * 1024);
+        if ((int)c * 8 >= d) continue;
+        if (whole) {
+            dma16(first, (reverse ? kChunk - 1 - row : row) * (u32)sl + c * 16, lds + part * 1024);
+        } else {
+            const int t = t0 + (int)row;
+            dma16(t < n ? x + walk(t, n, reverse) * sl + c * 16 : (const unsigned char*)kAbsent.zero,
+                  lds + part * 1024);
+        }
     }
 }
 
@@ -90,19 +99,35 @@ __global__ __launch_bounds__(DVP * 2, 2) void linear_kernel(const LinParams a)
     const u32 lds = (u32)(uintptr_t)(lds_byte*)smem;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), h = lane >> 5, col = lane & 31;
 
-    const int id = blockIdx.x;
-    const int seg = id % a.nseg, hd = id / a.nseg % a.H, b = id / a.nseg / a.H % a.B;
-    const LinJob& J = a.job[id / a.nseg / a.H / a.B];
+    // Segments from the last to the first for the outputs: the states' pass has
+    // left the last ones in the caches.
+    const int id = MODE == kOutputs ? (int)(gridDim.x - 1 - blockIdx.x) : (int)blockIdx.x;
+    const int hd = id % a.H, seg = id / a.H % a.nseg, b = id / a.H / a.nseg % a.B;
+    const LinJob J = a.job[id / a.H / a.nseg / a.B];
     const int n = uniform(a.lens ? min(max(a.lens[b], 0), a.L) : a.L);
     const bool reverse = J.reverse;
     const float g = fmaxf(a.log_decay[hd], -1e4f) * kLog2e;  // a^n is 0 for every n >= 1 below
-    const int t_begin = seg * a.seg_len, t_end = min(a.L, t_begin + a.seg_len), t_live = min(t_end, n);
+    const int t_end = min(a.L, (seg + 1) * a.seg_len), t_live = min(t_end, n);
+    int t_begin = seg * a.seg_len;
+    // Tokens whose decay to the segment's end is 0 in 32 bits add nothing to
+    // its own state.
+    if (MODE == kStates && g < 0) {
+        const int reach = (int)fminf(150.0f / -g, 1e9f) + 1;
+        t_begin = max(t_begin, t_begin + (t_live - reach - t_begin) / kChunk * kChunk);
+    }
 
+    const unsigned char* const xk = J.k.p + b * J.k.sb + hd * J.k.sh;
+    const unsigned char* const xv = J.v.p + b * J.v.sb + hd * J.v.sh;
+    const unsigned char* const xq = J.q.p + b * J.q.sb + hd * J.q.sh;
     const auto stage = [&](int t, u32 at) {
-        stage_tokens<LK, NW>(J.k, b, hd, J.dk, t, n, reverse, at);
-        stage_tokens<LV, NW>(J.v, b, hd, J.dv, t, n, reverse, at + TK);
-        if (OUT) stage_tokens<LK, NW>(J.q, b, hd, J.dk, t, n, reverse, at + TK + TV);
+        stage_tokens<LK, NW>(xk, J.k.sl, J.dk, t, n, reverse, at);
+        stage_tokens<LV, NW>(xv, J.v.sl, J.dv, t, n, reverse, at + TK);
+        if (OUT) stage_tokens<LK, NW>(xq, J.q.sl, J.dk, t, n, reverse, at + TK + TV);
     };
+    if (J.dk != LK || J.dv != LV) {
+        for (int at = threadIdx.x * 16; at < 2 * BUF; at += NW * 1024) lds_write16(lds + at, u32x4_t{});
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    }
     if (t_begin < t_live) stage(t_begin, lds);
 
     // The state: from the workspace in register order, or the one given.
@@ -146,6 +171,8 @@ __global__ __launch_bounds__(DVP * 2, 2) void linear_kernel(const LinParams a)
     };
     set_to_end(kChunk);
 
+    settle_loads();
+
     int t = t_begin;
     for (int it = 0; t < t_live; t += kChunk, ++it) {
         const u32 kt = lds + (it & 1) * BUF, vt = kt + TK, qt = vt + TV;
@@ -175,6 +202,15 @@ __global__ __launch_bounds__(DVP * 2, 2) void linear_kernel(const LinParams a)
                 for (int j = 0; j < 4; ++j)
                     sp[j] = pack2<BF>(S[ks / 2][(ks % 2) * 8 + 2 * j], S[ks / 2][(ks % 2) * 8 + 2 * j + 1]);
                 o = mfma<BF>(sp, q[ks], o);
+            }
+            // The first operands, then a product, the reads of a later one and
+            // the state's rounding in turn.
+            __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);
+#pragma unroll
+            for (int ks = 0; ks < 2 * KS; ++ks) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+                __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);
             }
             o *= from_start;
 #pragma unroll
@@ -255,11 +291,19 @@ __global__ __launch_bounds__(256) void linear_join_kernel(const LinParams a)
     const float g = fmaxf(a.log_decay[hd], -1e4f) * kLog2e;
     float T = real && J.s_in ? J.s_in[at] : 0.0f;
     float* x = J.seg + (int64_t)bh * a.nseg * PER + e;
-    for (int s = 0; s < a.nseg; ++s, x += PER) {
-        const int tokens = min(max(n - s * a.seg_len, 0), a.seg_len);
-        const float own = *x;
-        *x = T;
-        T = fmaf(T, __builtin_amdgcn_exp2f(g * (float)tokens), own);
+    constexpr int U = 8;  // segments in flight
+    for (int s = 0; s < a.nseg; s += U) {
+        float own[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (s + u < a.nseg) own[u] = x[(int64_t)(s + u) * PER];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (s + u >= a.nseg) break;
+            const int tokens = min(max(n - (s + u) * a.seg_len, 0), a.seg_len);
+            x[(int64_t)(s + u) * PER] = T;
+            T = fmaf(T, __builtin_amdgcn_exp2f(g * (float)tokens), own[u]);
+        }
     }
     if (real && J.s_out) J.s_out[at] = T;
 }
