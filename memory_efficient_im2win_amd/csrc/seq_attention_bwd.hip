@@ -116,7 +116,8 @@ struct RowStage {
         // Lanes 0-7: 32 values of lse, 8-15: of D.
         stat = (lane & 8 ? a.stat_delta : a.stat_lse) + (int64_t)bh * a.stat_rows + r0 + (lane & 7) * 4;
     }
-    // The next tile, to lds (q), lds + TILE (dout), lds + 2 * TILE (statistics).
+    // The next tile, to lds (q), lds + TILE (dout), lds + 2 * TILE
+    // (statistics). A wave that copies rows issues 2 * N loads, wave 0 one more.
     __device__ __forceinline__ void copy(u32 lds)
     {
         const unsigned char* zero = (const unsigned char*)kAbsent.zero;
@@ -133,7 +134,7 @@ struct RowStage {
             q[j] += step_q + (over ? wrap_q : 0);
             d[j] += step_d + (over ? wrap_d : 0);
         }
-        if (wave == NW - 1 && lane < 16) dma16(stat, lds + 2 * TILE);
+        if (wave == 0 && lane < 16) dma16(stat, lds + 2 * TILE);
         stat += kRowTile;
         r += kRowTile;
     }
@@ -150,12 +151,12 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_dkv_kernel(const AttnParams a
 {
     constexpr int LP = row_pitch(DP), KS = DP / 16, MT = DP / 32, TILE = kRowTile * LP * 2, STAT = 1024;
     constexpr int KEYS = NW * 16, BUF = 2 * TILE + STAT, HAND = 4096;  // row tiles of q and dout; P of 32 rows and keys
-    __shared__ __align__(1024) unsigned char smem[3 * BUF + NW * HAND];
+    __shared__ __align__(1024) unsigned char smem[4 * BUF + NW * HAND];
     const u32 lds = (u32)(uintptr_t)(lds_byte*)smem;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), h = lane >> 5;
     const int block = wave >> 1;
     const bool second = wave & 1;
-    const u32 hand = lds + 3 * BUF + block * (2 * HAND) + lane * 16;
+    const u32 hand = lds + 4 * BUF + block * (2 * HAND) + lane * 16;
 
     const int extras = a.sink_tiles * a.chunks, heads = a.B * a.Hkv;
     int id = blockIdx.x, tile, chunk = -1, bh;
@@ -188,6 +189,7 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_dkv_kernel(const AttnParams a
 
     RowStage<LP, NW> stage(a, b, hk, bh, rt0, r_end);
     if (n > 0) stage.copy(lds);
+    if (n > 1) stage.copy(lds + BUF);
     const Tensor& mine = second ? a.v : a.k;
     u32x4_t kv[KS];
 #pragma unroll
@@ -197,25 +199,29 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_dkv_kernel(const AttnParams a
                                                          : (const unsigned char*)kAbsent.zero);
     }
     settle_loads();
+    // The flattened rows that see this lane's key, from lo up to hi (a key at
+    // position j is seen from row (j - off) G on, for window * G rows; a sink to
+    // the end), and the same of every key of the wave and of any.
+    const int64_t row_of = (int64_t)(key - s.off) * a.G, row_of0 = (int64_t)(kw - s.off) * a.G;
+    const int64_t reach = (int64_t)a.window * a.G, more = 31 * (int64_t)a.G;
+    const auto in_walk = [&](int64_t x) { return (int)min(max(x, (int64_t)r_first), (int64_t)r_end); };
+    const int lo = in_walk(row_of), hi = key < a.sinks ? r_end : in_walk(row_of + reach);
+    const int all_lo = in_walk(row_of0 + more), all_hi = in_walk(row_of0 + reach);
+    const int any_lo = in_walk(row_of0), any_hi = kw < a.sinks ? r_end : in_walk(row_of0 + more + reach);
     const float c = a.scale * kLog2e;
     constexpr float kLift = BF ? 0.0f : 14.0f;  // log2 of P's factor
     Lift<BF> lift;
     floatx16_t acc[MT] = {};
-    int at = 0, before = 2;  // this tile's buffer, the last one's
+    // Four buffers: the tile before (second waves), this one, and two on their way.
     for (int t = 0; t <= n; ++t) {
-        const int next = 3 - at - before;
-        sync_all();
-        if (t + 1 < n) stage.copy(lds + next * BUF);
+        if (t + 1 < n) sync_but<2 * RowStage<LP, NW>::N>();
+        else sync_all();
+        if (t + 2 < n) stage.copy(lds + ((t + 2) & 3) * BUF);
         const int mt_ = second ? t - 1 : t;
-        const u32 buf = lds + (second ? before : at) * BUF;
-        const u32 to = hand + (mt_ & 1) * HAND;
-        before = at;
-        at = next;
+        const u32 buf = lds + (mt_ & 3) * BUF, to = hand + (mt_ & 1) * HAND;
         if (mt_ < 0 || mt_ >= n) continue;
-        const int rt = rt0 + mt_ * kRowTile, rb = min(rt + kRowTile, r_end) - 1;
-        const int pa = s.off + (int)a.by_group.div(rt), pb = s.off + (int)a.by_group.div(rb);
-        // Nothing here is seen by these keys.
-        if (pb < kw || (pa - (kw + 31) >= a.window && kw >= a.sinks)) continue;
+        const int rt = rt0 + mt_ * kRowTile;
+        if (rt >= any_hi || rt + kRowTile <= any_lo) continue;
         const RowsOf<LP> rows(buf + (second ? TILE : 0), lane & 31);
         const ColsOf<LP> cols(buf + (second ? 0 : TILE));
         floatx16_t x = {};
@@ -229,12 +235,13 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_dkv_kernel(const AttnParams a
         if (!second) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) x[i] = fmaf(x[i], c, kLift - st[i / 4][i % 4]);
-            if (!(pa >= kw + 31 && pb - kw < a.window && rt >= r_first && rt + kRowTile <= r_end)) {
+            if (rt < all_lo || rt + kRowTile > all_hi) {
+                int from = lo - rt - 4 * h, to_row = hi - rt - 4 * h;
+                asm("" : "+v"(from), "+v"(to_row));  // one pair of numbers, not one a register
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const int r = rt + 8 * (i / 4) + 4 * h + i % 4, p = s.off + (int)a.by_group.div(r);
-                    const bool seen = r >= r_first && r < r_end && key <= p && (p - key < a.window || key < a.sinks);
-                    x[i] = seen ? x[i] : -INFINITY;
+                    const int r = 8 * (i / 4) + i % 4;
+                    x[i] = r >= from && r < to_row ? x[i] : -INFINITY;
                 }
             }
 #pragma unroll
@@ -459,7 +466,7 @@ int run(AttnParams a, int group_keys, hipStream_t st)
 
 }  // namespace
 
-// Groups of 128 keys where they fill the card's 256 CUs, else of 64.
+// Groups of 128 keys where they come to half of the card's 256 CUs, else of 64.
 // Sink keys' rows past the window are cut into chunks of about 512 flattened
 // rows, so that they are spread over the card, as long as that makes no more
 // than 256 workgroups; no chunk walks further than the window's own walk
@@ -468,7 +475,7 @@ AttnBwdPlan attn_bwd_plan(const AttnParams& a)
 {
     AttnBwdPlan p{};
     p.stat_rows = ceil_div(a.rows, kRowTile) * kRowTile + kRowTile;
-    p.group_keys = (int64_t)a.B * a.Hkv * ceil_div(a.Lk, 128) >= 256 ? 128 : 64;
+    p.group_keys = (int64_t)a.B * a.Hkv * ceil_div(a.Lk, 128) >= 128 ? 128 : 64;
     p.key_tiles = ceil_div(a.Lk, p.group_keys);
     // Positions past the first key tile's window, if any key there is a sink.
     const int64_t past = (int64_t)a.Lk - (p.group_keys - 1) - a.window;

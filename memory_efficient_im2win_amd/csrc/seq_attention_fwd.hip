@@ -250,8 +250,9 @@ int run(const AttnParams& a, hipStream_t st)
 }  // namespace
 
 // Tiles of 128 rows where they fill the card's 256 CUs, else of 32; where even
-// those leave it idle, the keys are split until 512 workgroups are there or a
-// workgroup is down to one key tile.
+// those leave it idle and walk more than 4 key tiles, the keys are split until
+// 512 workgroups are there or a workgroup is down to one key tile. (A short
+// walk ends before a second launch would join its parts.)
 AttnPlan attn_plan(const AttnParams& a)
 {
     AttnPlan p{};
@@ -261,7 +262,7 @@ AttnPlan attn_plan(const AttnParams& a)
     const int64_t groups = heads * p.tiles;
     const int64_t keys = std::min<int64_t>((int64_t)a.window + p.waves * 32 / a.G, a.Lk) + std::min(a.sinks, a.Lk);
     const int64_t most = std::max<int64_t>(1, (keys + kKeyTile - 1) / kKeyTile);
-    p.nsplit = p.waves == 4 ? 1 : (int)std::min<int64_t>(most, (512 + groups - 1) / groups);
+    p.nsplit = p.waves == 4 || most <= 4 ? 1 : (int)std::min<int64_t>(most, (512 + groups - 1) / groups);
     p.ws_bytes = p.nsplit > 1 ? (size_t)p.nsplit * heads * a.rows * (a.D + 2) * 4 : 0;
     return p;
 }

@@ -108,6 +108,13 @@ __device__ __forceinline__ void sync_all()
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
+// The same with this wave's N youngest loads left under way.
+template <int N>
+__device__ __forceinline__ void sync_but()
+{
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
 // Elements of an LDS row for a head size padded to DP.
 __host__ __device__ constexpr int row_pitch(int DP) { return DP <= 64 ? 64 : 128; }
 

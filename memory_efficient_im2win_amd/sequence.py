@@ -22,6 +22,7 @@ needs from torch's allocator.
 """
 from __future__ import annotations
 
+import functools
 import struct
 
 from . import _lib
@@ -34,35 +35,55 @@ __all__ = ["window_attention", "window_attention_backward", "window_attention_wo
 _ATTENTION = struct.Struct("<16q5q11if16q")
 _LINEAR = struct.Struct("<16q4q6if4x16q2q")
 _NONE = (0, 0, 0, 0)
-_torch = None
+_NO_GRADS = _NONE * 4
+_NO_TAIL = _NO_GRADS + (0, 0)
+_torch = _raw_stream = None
 
 
 def _dtype_code(t):
-    global _torch
+    global _torch, _raw_stream
     if _torch is None:
         import torch
+        # torch.cuda.current_stream(device).cuda_stream without the object in
+        # between, which costs as much as the rest of a call's checks.
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda index: torch.cuda.current_stream(index).cuda_stream)
         _torch = torch
-    if t.dtype is _torch.bfloat16:
+    dtype = t.dtype
+    if dtype is _torch.bfloat16:
         return 1
-    if t.dtype is _torch.float16:
+    if dtype is _torch.float16:
         return 0
-    raise TypeError(f"expected float16 or bfloat16 tensors, got {t.dtype}")
+    raise TypeError(f"expected float16 or bfloat16 tensors, got {dtype}")
 
 
 def _tensor(t, name, like, shape):
-    """(pointer, batch, token and head stride) of a 4-d 16-bit tensor."""
-    if tuple(t.shape) != shape:
+    """(pointer, batch, token and head stride) of a 16-bit tensor (batch,
+    token, head, size), or (batch, head, size) of single tokens."""
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
     if t.dtype is not like.dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {like.dtype}")
     if t.device != like.device:
         raise ValueError(f"{name} must be on {like.device}")
-    if t.numel() == 0:
-        return _NONE
-    sb, sl, sh, sd = t.stride()
-    B, L, H, _ = shape
+    if len(shape) == 4:
+        sb, sl, sh, sd = t.stride()
+        B, L, H, _ = shape
+        if L <= 1:
+            sl = 0
+            if L == 0:
+                return _NONE
+    else:
+        sb, sh, sd = t.stride()
+        B, H, _ = shape
+        sl = 0
     # The stride of an extent of one means nothing.
-    sb, sl, sh = sb if B > 1 else 0, sl if L > 1 else 0, sh if H > 1 else 0
+    if B <= 1:
+        sb = 0
+        if B == 0:
+            return _NONE
+    if H == 1:
+        sh = 0
     p = t.data_ptr()
     if sd != 1 or (sb | sl | sh) & 7 or p & 15 or sl >= 1 << 24:
         raise ValueError(f"{name} needs an innermost stride of 1, other strides that are multiples of 8 elements "
@@ -74,7 +95,10 @@ def _output(t, name, like, shape):
     """The output tensor given, or a new one, and its pointer and strides."""
     if t is None:
         t = _torch.empty(shape, dtype=like.dtype, device=like.device)
-        return t, (t.data_ptr(), shape[1] * shape[2] * shape[3], shape[2] * shape[3], shape[3])
+        if len(shape) == 3:
+            return t, (t.data_ptr(), shape[1] * shape[2], 0, shape[2])
+        head = shape[2] * shape[3]
+        return t, (t.data_ptr(), shape[1] * head, head, shape[3])
     r = _tensor(t, name, like, shape)
     if t.numel() and 0 in [s for s, n in zip(t.stride(), shape) if n > 1]:
         raise ValueError(f"{name} must not overlap itself")
@@ -102,27 +126,43 @@ def _floats(t, name, like, shape):
 
 
 def _call(name, args, like, ws, need):
-    """Runs entry point `name` with `need` bytes of scratch on like's device."""
+    """Runs entry point `name` with `need` bytes of scratch (None: it takes
+    none) on like's device."""
     device = like.device
     ptr, size = 0, 0
     if ws is not None:
         if not ws.is_cuda or not ws.is_contiguous() or ws.device != device:
             raise ValueError(f"ws must be a contiguous GPU tensor on {device}")
-        ptr, size = ws.data_ptr(), ws.numel() * ws.element_size()
-        if need == 0:
-            ptr, size = 0, 0
+        if need:
+            ptr, size = ws.data_ptr(), ws.numel() * ws.element_size()
     elif need:
         ws = _torch.empty(need, dtype=_torch.uint8, device=device)
         ptr, size = ws.data_ptr(), need
-    stream = _torch.cuda.current_stream(device).cuda_stream
+    stream = _raw_stream(device.index)
+    args = (args, stream) if need is None else (args, ptr, size, stream)
     fn = getattr(_lib.load(), name)
     if device.index == _torch.cuda.current_device():
-        status = fn(args, ptr, size, stream)
+        status = fn(*args)
     else:
         with _torch.cuda.device(device):
-            status = fn(args, ptr, size, stream)
+            status = fn(*args)
     if status:
         _lib.check(status, name)
+
+
+@functools.lru_cache(maxsize=1024)
+def _attention_bytes(B, Lq, Lk, Hq, Hkv, D, window, sinks, backward):
+    args = _ATTENTION.pack(*[0] * 21, 0, B, Lq, Lk, Hq, Hkv, D, 0, 0, window, sinks, 1.0, *[0] * 16)
+    L = _lib.load()
+    return (L.im2win_seq_attention_backward_workspace_bytes if backward
+            else L.im2win_seq_attention_workspace_bytes)(args)
+
+
+@functools.lru_cache(maxsize=1024)
+def _linear_bytes(B, L, H, Dk, Dv, backward):
+    args = _LINEAR.pack(*[0] * 20, 0, B, L, H, Dk, Dv, 1.0, *[0] * 18)
+    lib = _lib.load()
+    return (lib.im2win_seq_linear_backward_workspace_bytes if backward else lib.im2win_seq_linear_workspace_bytes)(args)
 
 
 def _gpu(t, name, dims=4):
@@ -134,8 +174,8 @@ def _gpu(t, name, dims=4):
 
 
 def _attention_args(q, k, v, window, sinks, scale, q_lens, kv_lens, page_table):
-    """The packed argument up to the outputs: a function of (out, lse, grads),
-    and the shapes of q and of k and v."""
+    """The packed argument up to the outputs, a function of (out, lse, grads),
+    the shapes of q and of k and v, and the sizes that scratch memory goes by."""
     code = _gpu(q, "q")
     if k.dim() != 4:
         raise ValueError("k must have 4 dimensions")
@@ -171,12 +211,13 @@ def _attention_args(q, k, v, window, sinks, scale, q_lens, kv_lens, page_table):
     tq, tk, tv = _tensor(q, "q", q, (B, Lq, Hq, D)), _tensor(k, "k", q, kv_shape), _tensor(v, "v", q, kv_shape)
     lens = _ints(q_lens, "q_lens", q, (B,)), _ints(kv_lens, "kv_lens", q, (B,))
 
-    def pack(out, lse, dout=_NONE, dq=_NONE, dk=_NONE, dv=_NONE):
-        return _ATTENTION.pack(*tq, *tk, *tv, *out, lse, *lens, table, table_stride, code, B, Lq, Lk, Hq, Hkv, D,
-                               page, pages, min(window, 2**31 - 1), min(sinks, 2**31 - 1), scale,
-                               *dout, *dq, *dk, *dv)
+    window, sinks = min(window, 2**31 - 1), min(sinks, 2**31 - 1)
 
-    return pack, (B, Lq, Hq, D), kv_shape
+    def pack(out, lse, grads=_NO_GRADS):
+        return _ATTENTION.pack(*tq, *tk, *tv, *out, lse, *lens, table, table_stride, code, B, Lq, Lk, Hq, Hkv, D,
+                               page, pages, window, sinks, scale, *grads)
+
+    return pack, (B, Lq, Hq, D), kv_shape, (B, Lq, Lk, Hq, Hkv, D, window, sinks)
 
 
 def window_attention(q, k, v, *, window=None, sinks=0, scale=None, q_lens=None, kv_lens=None, page_table=None,
@@ -199,7 +240,7 @@ def window_attention(q, k, v, *, window=None, sinks=0, scale=None, q_lens=None, 
     pages may be gone. A page number outside the pool makes the outputs that
     need it NaN.
     """
-    pack, q_shape, _ = _attention_args(q, k, v, window, sinks, scale, q_lens, kv_lens, page_table)
+    pack, q_shape, _, sizes = _attention_args(q, k, v, window, sinks, scale, q_lens, kv_lens, page_table)
     out, t = _output(out, "out", q, q_shape)
     B, Lq, Hq, _ = q_shape
     p = 0
@@ -207,8 +248,7 @@ def window_attention(q, k, v, *, window=None, sinks=0, scale=None, q_lens=None, 
         if lse is None:
             lse = _torch.empty((B, Hq, Lq), dtype=_torch.float32, device=q.device)
         p = _floats(lse, "lse", q, (B, Hq, Lq))
-    args = pack(t, p)
-    _call("im2win_seq_attention", args, q, ws, _lib.load().im2win_seq_attention_workspace_bytes(args))
+    _call("im2win_seq_attention", pack(t, p), q, ws, _attention_bytes(*sizes, False))
     return (out, lse) if return_lse else out
 
 
@@ -217,7 +257,7 @@ def window_attention_backward(dout, q, k, v, out, lse, *, window=None, sinks=0, 
     """(dq, dk, dv) of window_attention without pages, from the gradient of its
     output and the ``out`` and ``lse`` that it returned. What lies past a
     sequence's end gets zeros."""
-    pack, q_shape, kv_shape = _attention_args(q, k, v, window, sinks, scale, q_lens, kv_lens, None)
+    pack, q_shape, kv_shape, sizes = _attention_args(q, k, v, window, sinks, scale, q_lens, kv_lens, None)
     B, Lq, Hq, _ = q_shape
     tout, tdout = _tensor(out, "out", q, q_shape), _tensor(dout, "dout", q, q_shape)
     if lse is None:
@@ -226,9 +266,7 @@ def window_attention_backward(dout, q, k, v, out, lse, *, window=None, sinks=0, 
     dq, a = _output(dq, "dq", q, q_shape)
     dk, b = _output(dk, "dk", q, kv_shape)
     dv, c = _output(dv, "dv", q, kv_shape)
-    args = pack(tout, p, tdout, a, b, c)
-    _call("im2win_seq_attention_backward", args, q, ws,
-          _lib.load().im2win_seq_attention_backward_workspace_bytes(args))
+    _call("im2win_seq_attention_backward", pack(tout, p, (*tdout, *a, *b, *c)), q, ws, _attention_bytes(*sizes, True))
     return dq, dk, dv
 
 
@@ -236,10 +274,7 @@ def window_attention_workspace_bytes(B, Lq, Lk, Hq, Hkv, D, window=None, sinks=0
     """Scratch bytes of window_attention, or of its backward call, for these
     sizes (Lk: the table's pages times their size for a paged cache)."""
     window = max(Lk, 1) if window is None else int(window)
-    args = _ATTENTION.pack(*[0] * 21, 0, B, Lq, Lk, Hq, Hkv, D, 0, 0, window, sinks, 1.0, *[0] * 16)
-    L = _lib.load()
-    return (L.im2win_seq_attention_backward_workspace_bytes if backward
-            else L.im2win_seq_attention_workspace_bytes)(args)
+    return _attention_bytes(B, Lq, Lk, Hq, Hkv, D, window, sinks, bool(backward))
 
 
 def _linear_sizes(q, k, v, log_decay, scale, dims):
@@ -282,8 +317,8 @@ def linear_attention(q, k, v, log_decay, *, state=None, scale=None, lens=None, o
         state_out = _torch.empty(st, dtype=_torch.float32, device=q.device)
     args = _LINEAR.pack(*_tensor(q, "q", q, qk), *_tensor(k, "k", q, qk), *_tensor(v, "v", q, vo), *t, decay,
                         _floats(state, "state", q, st), _floats(state_out, "state_out", q, st),
-                        _ints(lens, "lens", q, (B,)), code, B, L, H, Dk, Dv, scale, *[0] * 18)
-    _call("im2win_seq_linear", args, q, ws, _lib.load().im2win_seq_linear_workspace_bytes(args))
+                        _ints(lens, "lens", q, (B,)), code, B, L, H, Dk, Dv, scale, *_NO_TAIL)
+    _call("im2win_seq_linear", args, q, ws, _linear_bytes(B, L, H, Dk, Dv, False))
     return out, state_out
 
 
@@ -294,27 +329,13 @@ def linear_attention_step(q, k, v, log_decay, state, *, scale=None, out=None):
     B = q.shape[0]
     if state is None:
         raise ValueError("state is needed")
-    if out is None:
-        out = _torch.empty((B, H, Dv), dtype=q.dtype, device=q.device)
-    elif out.dim() != 3:
-        raise ValueError("out must have 3 dimensions")
-    if k.dim() != 3:
-        raise ValueError("k must have 3 dimensions")
-    t = [_tensor(x.unsqueeze(1), n, q, (B, 1, H, d))
-         for x, n, d in ((q, "q", Dk), (k, "k", Dk), (v, "v", Dv), (out, "out", Dv))]
+    qk, vo = (B, H, Dk), (B, H, Dv)
+    out, t = _output(out, "out", q, vo)
     s = _floats(state, "state", q, (B, H, Dk, Dv))
-    args = _LINEAR.pack(*t[0], *t[1], *t[2], *t[3], decay, s, s, 0, code, B, 1, H, Dk, Dv, scale, *[0] * 18)
-    _step(args, q)
+    args = _LINEAR.pack(*_tensor(q, "q", q, qk), *_tensor(k, "k", q, qk), *_tensor(v, "v", q, vo), *t, decay, s, s, 0,
+                        code, B, 1, H, Dk, Dv, scale, *_NO_TAIL)
+    _call("im2win_seq_linear_step", args, q, None, None)
     return out
-
-
-def _step(args, like):
-    device = like.device
-    stream = _torch.cuda.current_stream(device).cuda_stream
-    with _torch.cuda.device(device):
-        status = _lib.load().im2win_seq_linear_step(args, stream)
-    if status:
-        _lib.check(status, "im2win_seq_linear_step")
 
 
 def linear_attention_backward(dout, q, k, v, log_decay, *, state=None, dstate=None, scale=None, lens=None,
@@ -338,12 +359,10 @@ def linear_attention_backward(dout, q, k, v, log_decay, *, state=None, dstate=No
     args = _LINEAR.pack(*tq, *tk, *tv, *_NONE, decay, _floats(state, "state", q, st), 0, _ints(lens, "lens", q, (B,)),
                         code, B, L, H, Dk, Dv, scale, *tdout, *a, *b, *c, _floats(dstate, "dstate", q, st),
                         _floats(dstate_in, "dstate_in", q, st))
-    _call("im2win_seq_linear_backward", args, q, ws, _lib.load().im2win_seq_linear_backward_workspace_bytes(args))
+    _call("im2win_seq_linear_backward", args, q, ws, _linear_bytes(B, L, H, Dk, Dv, True))
     return dq, dk, dv, dstate_in
 
 
 def linear_attention_workspace_bytes(B, L, H, Dk, Dv, backward=False):
     """Scratch bytes of linear_attention, or of its backward call."""
-    args = _LINEAR.pack(*[0] * 20, 0, B, L, H, Dk, Dv, 1.0, *[0] * 18)
-    lib = _lib.load()
-    return (lib.im2win_seq_linear_backward_workspace_bytes if backward else lib.im2win_seq_linear_workspace_bytes)(args)
+    return _linear_bytes(B, L, H, Dk, Dv, bool(backward))
