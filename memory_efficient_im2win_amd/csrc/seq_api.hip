@@ -114,21 +114,25 @@ LinParams linear_params(const seq_linear* a, int jobs, const LinPlan& plan)
     return p;
 }
 
-// The recurrences of a backward call: dq and dk, whose states are dv x dk, in
-// one launch, dv in another.
+// The recurrences of a backward call: dq on its own; dk and dv over the same
+// tensors together where both heads pad to one size, else dk beside dq, whose
+// states are dv x dk too, and dv on its own.
 struct BackwardPlan {
-    LinPlan first, second;
-    size_t dq_bytes, dv_bytes, ws_bytes;
+    bool pair;
+    LinPlan dq, dk, dv;
+    size_t dq_bytes, dk_bytes, ws_bytes;
 };
 
 BackwardPlan backward_plan(const seq_linear* a)
 {
     BackwardPlan p{};
-    p.first = im2win::seq::lin_plan(2, a->B, a->L, a->H);
-    p.second = im2win::seq::lin_plan(1, a->B, a->L, a->H);
-    p.dq_bytes = im2win::seq::lin_seg_bytes(p.first, a->B, a->H, a->Dv, a->Dk);
-    p.dv_bytes = im2win::seq::lin_seg_bytes(p.second, a->B, a->H, a->Dk, a->Dv);
-    p.ws_bytes = 2 * p.dq_bytes + p.dv_bytes;
+    p.pair = im2win::seq::padded_head(a->Dk) == im2win::seq::padded_head(a->Dv);
+    p.dq = im2win::seq::lin_plan(p.pair ? 1 : 2, a->B, a->L, a->H);
+    p.dv = im2win::seq::lin_plan(p.pair ? 2 : 1, a->B, a->L, a->H);
+    p.dk = p.pair ? p.dv : p.dq;
+    p.dq_bytes = im2win::seq::lin_seg_bytes(p.dq, a->B, a->H, a->Dv, a->Dk);
+    p.dk_bytes = im2win::seq::lin_seg_bytes(p.dk, a->B, a->H, a->Dv, a->Dk);
+    p.ws_bytes = p.dq_bytes + p.dk_bytes + im2win::seq::lin_seg_bytes(p.dv, a->B, a->H, a->Dk, a->Dv);
     return p;
 }
 
@@ -194,7 +198,7 @@ int im2win_seq_linear(const seq_linear* a, void* ws, size_t ws_bytes, void* stre
     LinParams p = linear_params(a, 1, plan);
     p.job[0] = LinJob{tensor(a->q), tensor(a->k), tensor(a->v), tensor(a->out), a->state_in, a->state_out,
                       a->Dv, 1, a->Dk, a->Dv, 0, 1, a->scale, a->scale, 1.0f, static_cast<float*>(ws)};
-    return status_of(im2win::seq::launch_linear(p, a->dtype == 1, static_cast<hipStream_t>(stream)));
+    return status_of(im2win::seq::launch_linear(p, false, a->dtype == 1, static_cast<hipStream_t>(stream)));
 }
 
 int im2win_seq_linear_step(const seq_linear* a, void* stream)
@@ -228,17 +232,21 @@ int im2win_seq_linear_backward(const seq_linear* a, void* ws, size_t ws_bytes, v
     hipStream_t s = static_cast<hipStream_t>(stream);
     const Tensor q = tensor(a->q), k = tensor(a->k), v = tensor(a->v), dout = tensor(a->dout);
     // The states are transposed (rows dv, columns dk) for dq and dk.
-    LinParams p = linear_params(a, 2, plan.first);
-    p.job[0] = LinJob{dout, v, k, tensor(a->dq), a->state_in, nullptr, 1, a->Dv, a->Dv, a->Dk, 0, 1,
-                      a->scale, a->scale, 1.0f, reinterpret_cast<float*>(w)};
-    p.job[1] = LinJob{v, dout, q, tensor(a->dk), a->dstate_out, nullptr, 1, a->Dv, a->Dv, a->Dk, 1, 0,
-                      a->scale, 1.0f, a->scale, reinterpret_cast<float*>(w + plan.dq_bytes)};
-    int rc = im2win::seq::launch_linear(p, bf, s);
+    const LinJob dq{dout, v, k, tensor(a->dq), a->state_in, nullptr, 1, a->Dv, a->Dv, a->Dk, 0, 1,
+                    a->scale, a->scale, 1.0f, reinterpret_cast<float*>(w)};
+    const LinJob dk{v, dout, q, tensor(a->dk), a->dstate_out, nullptr, 1, a->Dv, a->Dv, a->Dk, 1, 0,
+                    a->scale, 1.0f, a->scale, reinterpret_cast<float*>(w + plan.dq_bytes)};
+    const LinJob dv{k, q, dout, tensor(a->dv), a->dstate_out, a->dstate_in, a->Dv, 1, a->Dk, a->Dv, 1, 0,
+                    a->scale, 1.0f, a->scale, reinterpret_cast<float*>(w + plan.dq_bytes + plan.dk_bytes)};
+    LinParams p = linear_params(a, plan.pair ? 1 : 2, plan.dq);
+    p.job[0] = dq;
+    p.job[1] = dk;
+    const int rc = im2win::seq::launch_linear(p, false, bf, s);
     if (rc != 0) return status_of(rc);
-    p = linear_params(a, 1, plan.second);
-    p.job[0] = LinJob{k, q, dout, tensor(a->dv), a->dstate_out, a->dstate_in, a->Dv, 1, a->Dk, a->Dv, 1, 0,
-                      a->scale, 1.0f, a->scale, reinterpret_cast<float*>(w + 2 * plan.dq_bytes)};
-    return status_of(im2win::seq::launch_linear(p, bf, s));
+    p = linear_params(a, plan.pair ? 2 : 1, plan.dv);
+    p.job[0] = plan.pair ? dk : dv;
+    p.job[1] = dv;
+    return status_of(im2win::seq::launch_linear(p, plan.pair, bf, s));
 }
 
 }  // extern "C"

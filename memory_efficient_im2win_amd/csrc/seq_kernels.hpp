@@ -83,8 +83,10 @@ struct LinPlan {
 };
 LinPlan lin_plan(int jobs, int B, int L, int H);
 size_t lin_seg_bytes(const LinPlan& p, int B, int H, int dk, int dv);
-// Jobs of one launch have the same head sizes.
-int launch_linear(const LinParams& a, bool bf, hipStream_t st);
+// Jobs of one launch have the same head sizes. pair: two jobs over the same
+// tensors, see seq_linear.hip; both head sizes pad to the same one.
+int launch_linear(const LinParams& a, bool pair, bool bf, hipStream_t st);
+int padded_head(int d);
 
 struct LinStep {
     Tensor q, k, v, out;

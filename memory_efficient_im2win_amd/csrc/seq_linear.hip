@@ -22,7 +22,7 @@
 // as q's operand, and v times its decay. The first two enter only `out`,
 // which is rounded to the same type. Decayed values enter the state, so they
 // are split into a sum of parts of the type (bf16: 3 parts, 24 bits; fp16: 2,
-// 22 bits) wherever the state goes on to another segment or to the caller.
+// 22 bits) where the caller asks for the last state; else they are rounded too.
 #include "seq_common.hpp"
 #include "seq_kernels.hpp"
 
@@ -32,7 +32,8 @@ namespace {
 
 constexpr int kChunk = 32;
 
-enum Mode { kStates, kOutputs, kWhole };
+enum Mode { kStates, kRoughStates, kOutputs, kWhole };
+constexpr bool has_outputs(int mode) { return mode >= kOutputs; }
 
 // Position of token t of the walk; absent tokens (t >= n) keep their place.
 __device__ __forceinline__ int walk(int t, int n, bool reverse) { return reverse && t < n ? n - 1 - t : t; }
@@ -88,22 +89,30 @@ __device__ __forceinline__ void split_parts(u32x4_t x, const float* w, u32x4_t* 
     }
 }
 
-template <bool BF, int DKP, int DVP, int MODE>
-__global__ __launch_bounds__(DVP * 2, 2) void linear_kernel(const LinParams a)
+// PAIR: two jobs side by side over the same tokens, DKP = DVP: the first one's
+// k and v are the second one's v and k, its q the second one's q in the third
+// tile's place, so that 4 tensors (2 for the states) are read in place of 6
+// (4). The first half of the waves takes the first job.
+template <bool BF, int DKP, int DVP, int MODE, bool PAIR>
+__global__ __launch_bounds__(DVP * (PAIR ? 4 : 2), 2) void linear_kernel(const LinParams a)
 {
-    constexpr int NW = DVP / 32, LK = row_pitch(DKP), LV = row_pitch(DVP), KS = DKP / 16, MT = DKP / 32;
-    constexpr int TK = kChunk * LK * 2, TV = kChunk * LV * 2, OUT = MODE != kStates;
-    constexpr int BUF = TK + TV + OUT * TK;  // k, v, q
-    constexpr int PARTS = MODE == kOutputs ? 1 : BF ? 3 : 2;
+    constexpr int NW = DVP / 32, ALL = PAIR ? 2 * NW : NW;
+    constexpr int LK = row_pitch(DKP), LV = row_pitch(DVP), KS = DKP / 16, MT = DKP / 32;
+    constexpr int TK = kChunk * LK * 2, TV = kChunk * LV * 2, OUT = has_outputs(MODE);
+    constexpr int BUF = TK + TV + OUT * (PAIR ? 2 : 1) * TK;  // k, v, q (and the second job's q)
+    constexpr int PARTS = MODE == kOutputs || MODE == kRoughStates ? 1 : BF ? 3 : 2;
     __shared__ __align__(1024) unsigned char smem[2 * BUF];
     const u32 lds = (u32)(uintptr_t)(lds_byte*)smem;
-    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), h = lane >> 5, col = lane & 31;
+    const int lane = threadIdx.x & 63, h = lane >> 5, col = lane & 31;
+    const int role = PAIR ? uniform(threadIdx.x >> 6) / NW : 0;
+    const int wave = uniform(threadIdx.x >> 6) - role * NW, thread = wave * 64 + lane;
 
     // Segments from the last to the first for the outputs: the states' pass has
     // left the last ones in the caches.
     const int id = MODE == kOutputs ? (int)(gridDim.x - 1 - blockIdx.x) : (int)blockIdx.x;
     const int hd = id % a.H, seg = id / a.H % a.nseg, b = id / a.H / a.nseg % a.B;
-    const LinJob J = a.job[id / a.H / a.nseg / a.B];
+    const LinJob& J0 = a.job[PAIR ? 0 : id / a.H / a.nseg / a.B];
+    const LinJob J = PAIR ? a.job[role] : J0;
     const int n = uniform(a.lens ? min(max(a.lens[b], 0), a.L) : a.L);
     const bool reverse = J.reverse;
     const float g = fmaxf(a.log_decay[hd], -1e4f) * kLog2e;  // a^n is 0 for every n >= 1 below
@@ -111,28 +120,31 @@ __global__ __launch_bounds__(DVP * 2, 2) void linear_kernel(const LinParams a)
     int t_begin = seg * a.seg_len;
     // Tokens whose decay to the segment's end is 0 in 32 bits add nothing to
     // its own state.
-    if (MODE == kStates && g < 0) {
+    if (!OUT && g < 0) {
         const int reach = (int)fminf(150.0f / -g, 1e9f) + 1;
         t_begin = max(t_begin, t_begin + (t_live - reach - t_begin) / kChunk * kChunk);
     }
 
-    const unsigned char* const xk = J.k.p + b * J.k.sb + hd * J.k.sh;
-    const unsigned char* const xv = J.v.p + b * J.v.sb + hd * J.v.sh;
-    const unsigned char* const xq = J.q.p + b * J.q.sb + hd * J.q.sh;
+    const auto head = [&](const Tensor& x) { return x.p + b * x.sb + hd * x.sh; };
+    const unsigned char *const xk = head(J0.k), *const xv = head(J0.v), *const xq = head(J0.q);
+    const unsigned char* const xq1 = PAIR ? head(a.job[1].q) : nullptr;
+    const int64_t slk = J0.k.sl, slv = J0.v.sl, slq = J0.q.sl, slq1 = PAIR ? a.job[1].q.sl : 0;
+    const int dk0 = J0.dk, dv0 = J0.dv;
     const auto stage = [&](int t, u32 at) {
-        stage_tokens<LK, NW>(xk, J.k.sl, J.dk, t, n, reverse, at);
-        stage_tokens<LV, NW>(xv, J.v.sl, J.dv, t, n, reverse, at + TK);
-        if (OUT) stage_tokens<LK, NW>(xq, J.q.sl, J.dk, t, n, reverse, at + TK + TV);
+        stage_tokens<LK, ALL>(xk, slk, dk0, t, n, reverse, at);
+        stage_tokens<LV, ALL>(xv, slv, dv0, t, n, reverse, at + TK);
+        if (OUT) stage_tokens<LK, ALL>(xq, slq, dk0, t, n, reverse, at + TK + TV);
+        if (OUT && PAIR) stage_tokens<LK, ALL>(xq1, slq1, dv0, t, n, reverse, at + TK + TV + TK);
     };
     if (J.dk != LK || J.dv != LV) {
-        for (int at = threadIdx.x * 16; at < 2 * BUF; at += NW * 1024) lds_write16(lds + at, u32x4_t{});
+        for (int at = threadIdx.x * 16; at < 2 * BUF; at += ALL * 1024) lds_write16(lds + at, u32x4_t{});
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     }
     if (t_begin < t_live) stage(t_begin, lds);
 
     // The state: from the workspace in register order, or the one given.
     floatx16_t S[MT] = {};
-    float* seg_state = J.seg + (((int64_t)b * a.H + hd) * a.nseg + seg) * (DKP * DVP) + threadIdx.x;
+    float* seg_state = J.seg + (((int64_t)b * a.H + hd) * a.nseg + seg) * (DKP * DVP) + thread;
     const int64_t given = ((int64_t)b * a.H + hd) * J.dk * J.dv;
     if (MODE == kOutputs) {
 #pragma unroll
@@ -175,7 +187,8 @@ __global__ __launch_bounds__(DVP * 2, 2) void linear_kernel(const LinParams a)
 
     int t = t_begin;
     for (int it = 0; t < t_live; t += kChunk, ++it) {
-        const u32 kt = lds + (it & 1) * BUF, vt = kt + TK, qt = vt + TV;
+        const u32 buf = lds + (it & 1) * BUF;
+        const u32 kt = buf + (role ? TK : 0), vt = buf + (role ? 0 : TK), qt = buf + TK + TV + (role ? TK : 0);
         const int tokens = min(kChunk, t_live - t);
         sync_all();
         if (t + kChunk < t_live) stage(t + kChunk, lds + ((it + 1) & 1) * BUF);
@@ -257,7 +270,7 @@ __global__ __launch_bounds__(DVP * 2, 2) void linear_kernel(const LinParams a)
             if (lane * 4 < J.dv) *(u32x2_t*)(out + lane * 8) = (u32x2_t)(0u);
         }
     }
-    if (MODE == kStates) {
+    if (!OUT) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -362,17 +375,21 @@ __global__ __launch_bounds__(256) void linear_step_kernel(const LinStep a, int c
     }
 }
 
-template <bool BF, int DKP, int DVP>
+template <bool BF, int DKP, int DVP, bool PAIR>
 int run(const LinParams& a, hipStream_t st)
 {
-    const unsigned heads = (unsigned)(a.jobs * a.B * a.H), grid = heads * (unsigned)a.nseg;
+    const unsigned heads = (unsigned)(a.B * a.H), all = heads * (unsigned)a.jobs;
+    const unsigned grid = (PAIR ? heads : all) * (unsigned)a.nseg, threads = DVP * (PAIR ? 4 : 2);
     if (a.nseg == 1) {
-        linear_kernel<BF, DKP, DVP, kWhole><<<grid, DVP * 2, 0, st>>>(a);
+        linear_kernel<BF, DKP, DVP, kWhole, PAIR><<<grid, threads, 0, st>>>(a);
         return launch_status();
     }
-    linear_kernel<BF, DKP, DVP, kStates><<<grid, DVP * 2, 0, st>>>(a);
-    linear_join_kernel<DKP, DVP><<<heads * (DKP * DVP / 256), 256, 0, st>>>(a);
-    linear_kernel<BF, DKP, DVP, kOutputs><<<grid, DVP * 2, 0, st>>>(a);
+    bool wanted = false;
+    for (int j = 0; j < a.jobs; ++j) wanted |= a.job[j].s_out != nullptr;
+    if (wanted) linear_kernel<BF, DKP, DVP, kStates, PAIR><<<grid, threads, 0, st>>>(a);
+    else linear_kernel<BF, DKP, DVP, kRoughStates, PAIR><<<grid, threads, 0, st>>>(a);
+    linear_join_kernel<DKP, DVP><<<all * (DKP * DVP / 256), 256, 0, st>>>(a);
+    linear_kernel<BF, DKP, DVP, kOutputs, PAIR><<<grid, threads, 0, st>>>(a);
     return launch_status();
 }
 
@@ -392,15 +409,21 @@ LinPlan lin_plan(int jobs, int B, int L, int H)
 size_t lin_seg_bytes(const LinPlan& p, int B, int H, int dk, int dv)
 {
     if (p.nseg == 1) return 0;
-    const auto pad = [](int d) { return with_head(d, [](auto D) { return (int)D.value; }); };
-    return (size_t)B * H * p.nseg * pad(dk) * pad(dv) * 4;
+    return (size_t)B * H * p.nseg * padded_head(dk) * padded_head(dv) * 4;
 }
 
-int launch_linear(const LinParams& a, bool bf, hipStream_t st)
+int padded_head(int d)
+{
+    return with_head(d, [](auto D) { return (int)D.value; });
+}
+
+int launch_linear(const LinParams& a, bool pair, bool bf, hipStream_t st)
 {
     return with_head(a.job[0].dk, [&](auto DK) {
+        if (pair)
+            return bf ? run<true, DK.value, DK.value, true>(a, st) : run<false, DK.value, DK.value, true>(a, st);
         return with_head(a.job[0].dv, [&](auto DV) {
-            return bf ? run<true, DK.value, DV.value>(a, st) : run<false, DK.value, DV.value>(a, st);
+            return bf ? run<true, DK.value, DV.value, false>(a, st) : run<false, DK.value, DV.value, false>(a, st);
         });
     });
 }
