@@ -55,10 +55,10 @@ struct Mask {
     __device__ __forceinline__ bool operator()(int i) const { return i <= near && (i > edge || i < sink); }
 };
 
-// Copies tiles of 64 keys or values into LDS. Keys that no row of the
-// workgroup sees arrive as zeros, so what they hold in memory does not matter;
-// those of a page outside the pool as NaN. Chunks past the head size are not
-// written: clear() zeroes them once.
+// Copies tiles of 64 keys or values into LDS, by NW waves of which the caller
+// is number `wave`. Keys that no row of the workgroup sees arrive as zeros, so
+// what they hold in memory does not matter; those of a page outside the pool as
+// NaN. Chunks past the head size are not written: clear() zeroes them once.
 template <int LP, int NW, bool PAGED>
 struct KeyStage {
     static constexpr int CH = LP / 8, RPI = 64 / CH, N = kKeyTile / RPI / NW, TILE = kKeyTile * LP * 2;
@@ -69,8 +69,8 @@ struct KeyStage {
     const KeyTiles& kt;
     int b, hk, lane, wave;
 
-    __device__ __forceinline__ KeyStage(const AttnParams& a_, const KeyTiles& kt_, int b_, int hk_)
-        : a(a_), kt(kt_), b(b_), hk(hk_), lane(threadIdx.x & 63), wave(uniform(threadIdx.x >> 6))
+    __device__ __forceinline__ KeyStage(const AttnParams& a_, const KeyTiles& kt_, int b_, int hk_, int wave_)
+        : a(a_), kt(kt_), b(b_), hk(hk_), lane(threadIdx.x & 63), wave(wave_)
     {
     }
     __device__ __forceinline__ u32 row(int j) const { return (j * NW + wave) * RPI + lane / CH; }
@@ -79,7 +79,7 @@ struct KeyStage {
     __device__ __forceinline__ static void clear(u32 lds, int bytes, int D)
     {
         if (D == LP) return;
-        for (int at = threadIdx.x * 16; at < bytes; at += NW * 1024) lds_write16(lds + at, (u32x4_t)(0u));
+        for (int at = threadIdx.x * 16; at < bytes; at += blockDim.x * 16) lds_write16(lds + at, (u32x4_t)(0u));
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     }
 
@@ -90,6 +90,15 @@ struct KeyStage {
 #pragma unroll
         for (int j = 0; j < N; ++j)
             p.id[j] = a.table[b * a.table_stride + a.by_page.div(min(t * kKeyTile + (int)row(j), kt.hi))];
+    }
+
+    // Tiles t of k and of v. The pages that were looked up are waited for once,
+    // before copies are under way that a wait for one of them would also wait for.
+    __device__ __forceinline__ void copy_both(int t, const Pages& p, u32 lds) const
+    {
+        if (PAGED) settle_loads();
+        copy(a.k, t, p, lds);
+        copy(a.v, t, p, lds + TILE);
     }
 
     // Tile t of x (k or v).
@@ -117,10 +126,29 @@ struct KeyStage {
             }
             return;
         }
-        // All pages at once, before copies are under way that a wait for one
-        // of them would also wait for.
-        settle_loads();
         const unsigned char* from = x.p + hk * x.sh;
+        const bool whole = k0 + kKeyTile - 1 <= kt.hi && (k0 >= kt.lo || k0 + kKeyTile <= a.sinks);
+        if (a.by_page.d % RPI == 0) {
+            // The rows of one copy lie in one page: its address is the same for the wave.
+            const u32 row_at = (lane / CH) * (u32)x.sl;
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const int id = uniform(p.id[j]), first = k0 + (j * NW + wave) * RPI;
+                const int at = first - (int)a.by_page.div(first) * (int)a.by_page.d;
+                const unsigned char* page = from + id * x.sb + at * x.sl;
+                const bool bad = (u32)id >= (u32)a.pages;
+                if ((int)chunk(j) * 8 >= a.D) continue;
+                if (whole && !bad) {
+                    dma16(page, row_at + chunk(j) * 16, lds + (j * NW + wave) * 1024);
+                } else {
+                    const int key = k0 + (int)row(j);
+                    const bool there = key <= kt.hi && (key >= kt.lo || key < a.sinks);
+                    const unsigned char* const e = bad ? (const unsigned char*)kAbsent.nan : page + row_at + chunk(j) * 16;
+                    dma16(there ? e : zero, lds + (j * NW + wave) * 1024);
+                }
+            }
+            return;
+        }
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             const int key = k0 + (int)row(j), at = key - (int)a.by_page.div(key) * (int)a.by_page.d;

@@ -1,10 +1,11 @@
 // Window attention, backward. With P = exp(S - lse) and D_i = dout_i . out_i,
 //     dS = P o (dout V^T - D),  dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dout.
 //
-// Three kernels: the row statistics; dK and dV with a wave owning 32 keys and
-// walking the rows that see them (the heads of a group are rows of one walk,
-// so shared heads are summed in registers, in a fixed order); dQ with a wave
-// owning 32 rows and walking their keys, as the forward pass does. P and dS
+// Two kernels: dQ with a wave owning 32 rows and walking their keys, as the
+// forward pass does, which leaves the rows' statistics for the other; dK and dV
+// with waves owning 32 keys and walking the rows that see them (the heads of a
+// group are rows of one walk, so shared heads are summed in registers, in a
+// fixed order). P and dS
 // are formed in both (7 products in place of 5), which needs no sums across
 // workgroups. P and dS are rounded to the element type as operands, half a step
 // each, independent from pair to pair. In fp16 they carry powers of two that
@@ -46,40 +47,6 @@ struct Lift {
     __device__ __forceinline__ float in() const { return BF ? 1.0f : f; }
     __device__ __forceinline__ float out() const { return BF || f == 0 ? 1.0f : 1.0f / f; }
 };
-
-// Row statistics: lse in log2 units (+infinity where a row sees nothing or is
-// padding, so that its P is 0) and D. 16 lanes a row.
-template <bool BF>
-__global__ __launch_bounds__(256) void attn_stat_kernel(const AttnParams a)
-{
-    const int64_t row = (int64_t)blockIdx.x * 16 + threadIdx.x / 16;
-    const int bh = (int)(row / a.stat_rows), r = (int)(row % a.stat_rows), lane = threadIdx.x & 15;
-    if (bh >= a.B * a.Hkv) return;
-    const int b = bh / a.Hkv, hk = bh % a.Hkv;
-    const Span s(a, b);
-    const int i = a.by_group.div(r), g = r - i * a.G;
-    float lse = INFINITY, d = 0;
-    if (r < a.rows && i < s.nq && s.off + i >= 0) {
-        for (int c = lane * 8; c < a.D; c += 128) {
-            const u32x4_t x = *(const u32x4_t*)row_ptr(a, a.out, b, hk, r, a.rows, c);
-            const u32x4_t y = *(const u32x4_t*)row_ptr(a, a.dout, b, hk, r, a.rows, c);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const floatx2_t u = unpack2<BF>(x[j]), v = unpack2<BF>(y[j]);
-                d = fmaf(u[0], v[0], d);
-                d = fmaf(u[1], v[1], d);
-            }
-        }
-        const float v = a.lse[((int64_t)b * a.Hq + hk * a.G + g) * a.Lq + i];
-        lse = v == -INFINITY ? INFINITY : v * kLog2e;
-    }
-#pragma unroll
-    for (int k = 8; k; k >>= 1) d += __shfl_xor(d, k, 16);
-    if (lane == 0) {
-        a.stat_lse[row] = lse;
-        a.stat_delta[row] = d;
-    }
-}
 
 // Copies tiles of 32 rows of q and dout and their statistics into LDS, the
 // rows in order from r0. Rows from r_end on arrive as zeros. The pointers move
@@ -336,7 +303,8 @@ __global__ __launch_bounds__(256) void attn_sink_join_kernel(const AttnParams a)
     *(u32x2_t*)(t.p + b * t.sb + key * t.sl + hk * t.sh + d * 2) = w;
 }
 
-// dQ of 128 flattened rows, 32 a wave.
+// dQ of 128 flattened rows, 32 a wave, and their statistics: lse in log2 units
+// (+infinity where a row sees nothing or is padding, so that its P is 0) and D.
 template <bool BF, int DP>
 __global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnParams a)
 {
@@ -354,35 +322,52 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnParams a)
     const int pw_lo = s.off + (int)a.by_group.div(rw), pw_hi = s.off + min((int)a.by_group.div(rw + 31), s.nq - 1);
     const int p = s.off + (int)a.by_group.div(r);
 
-    KeyStage<LP, NW, false> stage(a, kt, b, hk);
+    KeyStage<LP, NW, false> stage(a, kt, b, hk, wave);
     stage.clear(lds, 4 * TILE, a.D);
     const typename KeyStage<LP, NW, false>::Pages none{};
-    const auto copy = [&](int t, u32 at) {
-        stage.copy(a.k, t, none, at);
-        stage.copy(a.v, t, none, at + TILE);
-    };
-    if (kt.n > 0) copy(kt.at(0), lds);
+    if (kt.n > 0) stage.copy_both(kt.at(0), none, lds);
 
     u32x4_t q[KS], dout[KS];
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-        q[ks] = *(const u32x4_t*)row_ptr(a, a.q, b, hk, r, r_end, ks * 16 + h * 8);
-        dout[ks] = *(const u32x4_t*)row_ptr(a, a.dout, b, hk, r, r_end, ks * 16 + h * 8);
-    }
     float l2 = INFINITY, delta = 0;
-    if (r < a.rows) {
-        l2 = a.stat_lse[(int64_t)bh * a.stat_rows + r];
-        delta = a.stat_delta[(int64_t)bh * a.stat_rows + r];
+    {
+        u32x4_t out[KS];
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            q[ks] = *(const u32x4_t*)row_ptr(a, a.q, b, hk, r, r_end, ks * 16 + h * 8);
+            dout[ks] = *(const u32x4_t*)row_ptr(a, a.dout, b, hk, r, r_end, ks * 16 + h * 8);
+            out[ks] = *(const u32x4_t*)row_ptr(a, a.out, b, hk, r, r_end, ks * 16 + h * 8);
+        }
+        if (r < r_end && p >= 0) {
+            const int i = a.by_group.div(r), g = r - i * a.G;
+            const float v = a.lse[((int64_t)b * a.Hq + hk * a.G + g) * a.Lq + i];
+            l2 = v == -INFINITY ? INFINITY : v * kLog2e;
+        }
+        settle_loads();
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const floatx2_t u = unpack2<BF>(out[ks][j]), v = unpack2<BF>(dout[ks][j]);
+                delta = fmaf(u[0], v[0], delta);
+                delta = fmaf(u[1], v[1], delta);
+            }
+        delta = half_sum(delta);
+        if (p < 0) delta = 0;
+        float* const lse = a.stat_lse + (int64_t)bh * a.stat_rows;
+        float* const d = a.stat_delta + (int64_t)bh * a.stat_rows;
+        if (h == 0 && r < a.stat_rows) lse[r] = l2, d[r] = delta;
+        // Padding past the last tile of rows.
+        const int past = a.tiles * (NW * 32) + (int)threadIdx.x;
+        if (tile == a.tiles - 1 && past < a.stat_rows) lse[past] = INFINITY, d[past] = 0;
     }
     const float c = a.scale * kLog2e;
-    settle_loads();
 
     Lift<BF> lift;
     floatx16_t dq[MT] = {};
     for (int it = 0; it < kt.n; ++it) {
         const u32 buf = lds + (it & 1) * (2 * TILE), nbuf = lds + ((it + 1) & 1) * (2 * TILE);
         sync_all();
-        if (it + 1 < kt.n) copy(kt.at(it + 1), nbuf);
+        if (it + 1 < kt.n) stage.copy_both(kt.at(it + 1), none, nbuf);
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
             const int k0 = kt.at(it) * kKeyTile + kb * 32;
@@ -447,16 +432,13 @@ template <bool BF>
 int run(AttnParams a, int group_keys, hipStream_t st)
 {
     const int64_t heads = (int64_t)a.B * a.Hkv;
-    attn_stat_kernel<BF><<<(unsigned)((heads * a.stat_rows + 15) / 16), 256, 0, st>>>(a);
-    int rc = launch_status();
-    if (rc != 0) return rc;
     a.tiles = ceil_div(a.rows, 128);
-    rc = with_head(a.D, [&](auto DP) {
+    const int rc = with_head(a.D, [&](auto DP) {
+        if (a.tiles) attn_dq_kernel<BF, DP.value><<<(unsigned)(heads * a.tiles), 256, 0, st>>>(a);
         const int items = a.key_tiles + a.sink_tiles * a.chunks;
         const unsigned grid = (unsigned)(heads * items);
         if (items && group_keys == 128) attn_dkv_kernel<BF, DP.value, 8><<<grid, 512, 0, st>>>(a);
         else if (items) attn_dkv_kernel<BF, DP.value, 4><<<grid, 256, 0, st>>>(a);
-        if (a.tiles) attn_dq_kernel<BF, DP.value><<<(unsigned)(heads * a.tiles), 256, 0, st>>>(a);
         return launch_status();
     });
     if (rc != 0 || a.sink_tiles == 0) return rc;

@@ -14,8 +14,12 @@
 // terms carry a factor 2^6 more (below 2^14 still), which keeps small ones
 // out of the type's subnormal range.
 //
-// Key tiles go to LDS by direct loads, the next tile's under this tile's
-// products (two buffers, one barrier a tile).
+// Key tiles go to LDS by direct loads. Where there are many rows, four waves
+// of 32 rows each share the tiles, the next one's copy under this one's
+// products (two buffers, one barrier a tile). Where there are few, four waves
+// share 32 rows and take every fourth tile each into a buffer of their own, with no
+// barrier, and join at the end in a fixed order: a call that is too small to
+// fill the card is a chain of waits for memory, and this one is a quarter as long.
 #include <type_traits>
 
 #include "seq_attention.hpp"
@@ -24,11 +28,17 @@ namespace im2win {
 namespace seq {
 namespace {
 
-template <bool BF, int DP, int NW, bool PAGED>
-__global__ __launch_bounds__(NW * 64, NW > 2 ? 2 : 1) void attn_fwd_kernel(const AttnParams a)
+constexpr int kWaves = 4;
+
+// ROWS: the workgroup's rows, 32 a wave or 32 for all waves.
+template <bool BF, int DP, int ROWS, bool PAGED>
+__global__ __launch_bounds__(kWaves * 64, 2) void attn_fwd_kernel(const AttnParams a)
 {
+    constexpr bool APART = ROWS == 32;  // each wave walks its own tiles
+    constexpr int NW = APART ? 1 : kWaves;  // waves that share a tile
     constexpr int LP = row_pitch(DP), KS = DP / 16, MT = DP / 32, TILE = kKeyTile * LP * 2;
-    __shared__ __align__(1024) unsigned char smem[4 * TILE];
+    constexpr int BYTES = (APART ? kWaves : 2) * 2 * TILE;
+    __shared__ __align__(1024) unsigned char smem[BYTES];
     const u32 lds = (u32)(uintptr_t)(lds_byte*)smem;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), h = lane >> 5;
 
@@ -37,25 +47,26 @@ __global__ __launch_bounds__(NW * 64, NW > 2 ? 2 : 1) void attn_fwd_kernel(const
     const int b = bh / a.Hkv, hk = bh % a.Hkv;
     const Span s(a, b);
 
-    const int r0 = tile * (NW * 32), rw = r0 + wave * 32, r = rw + (lane & 31);
+    const int r0 = tile * ROWS, rw = r0 + (APART ? 0 : wave * 32), r = rw + (lane & 31);
     const int r_end = s.nq * a.G;  // rows past it are empty
-    const int i0 = a.by_group.div(r0), i1 = min((int)a.by_group.div(min(r0 + NW * 32, a.rows) - 1), s.nq - 1);
+    const int i0 = a.by_group.div(r0), i1 = min((int)a.by_group.div(min(r0 + ROWS, a.rows) - 1), s.nq - 1);
     const KeyTiles kt(a, s, i0, i1);
     const int per = (kt.n + a.nsplit - 1) / a.nsplit;
-    const int it0 = split * per, it1 = min(kt.n, it0 + per);
+    const int it1 = min(kt.n, (split + 1) * per), it0 = split * per + (APART ? wave : 0);
+    constexpr int STEP = APART ? kWaves : 1;
 
     // The positions of this wave's rows, and of this lane's.
     const int pw_lo = s.off + (int)a.by_group.div(rw), pw_hi = s.off + min((int)a.by_group.div(rw + 31), s.nq - 1);
     const int p = s.off + (int)a.by_group.div(r);
 
-    const KeyStage<LP, NW, PAGED> stage(a, kt, b, hk);
+    const KeyStage<LP, NW, PAGED> stage(a, kt, b, hk, APART ? 0 : wave);
     typename KeyStage<LP, NW, PAGED>::Pages ahead{};  // pages of the next tile
-    stage.clear(lds, 4 * TILE, a.D);
+    stage.clear(lds, BYTES, a.D);
+    const u32 mine = lds + (APART ? wave * (2 * TILE) : 0);
     if (it0 < it1) {
         stage.look_up(kt.at(it0), ahead);
-        stage.copy(a.k, kt.at(it0), ahead, lds);
-        stage.copy(a.v, kt.at(it0), ahead, lds + TILE);
-        if (it0 + 1 < it1) stage.look_up(kt.at(it0 + 1), ahead);
+        stage.copy_both(kt.at(it0), ahead, mine);
+        if (it0 + STEP < it1) stage.look_up(kt.at(it0 + STEP), ahead);
     }
 
     // A negative scale flips the rows' sign (exact), so that the largest
@@ -74,13 +85,22 @@ __global__ __launch_bounds__(NW * 64, NW > 2 ? 2 : 1) void attn_fwd_kernel(const
     floatx16_t o[MT] = {};
     constexpr float kLift = BF ? 0.0f : 6.0f;
     float m = -INFINITY, mc = 0, l = 0;  // reference, the same in log2 units, this lane's sum
-    for (int it = it0; it < it1; ++it) {
-        const u32 buf = lds + ((it - it0) & 1) * (2 * TILE), nbuf = lds + ((it - it0 + 1) & 1) * (2 * TILE);
-        sync_all();
-        if (it + 1 < it1) {
-            stage.copy(a.k, kt.at(it + 1), ahead, nbuf);
-            stage.copy(a.v, kt.at(it + 1), ahead, nbuf + TILE);
-            if (it + 2 < it1) stage.look_up(kt.at(it + 2), ahead);
+    for (int it = it0; it < it1; it += STEP) {
+        u32 buf = mine;
+        if (APART) {
+            if (it != it0) {
+                wait_reads();
+                stage.copy_both(kt.at(it), ahead, buf);
+                if (it + STEP < it1) stage.look_up(kt.at(it + STEP), ahead);
+            }
+            wait_copies();
+        } else {
+            buf = lds + ((it - it0) & 1) * (2 * TILE);
+            sync_all();
+            if (it + 1 < it1) {
+                stage.copy_both(kt.at(it + 1), ahead, lds + ((it - it0 + 1) & 1) * (2 * TILE));
+                if (it + 2 < it1) stage.look_up(kt.at(it + 2), ahead);
+            }
         }
         const int k0 = kt.at(it) * kKeyTile;
         if (rw >= r_end || k0 > pw_hi || (k0 + kKeyTile - 1 <= pw_lo - a.window && k0 >= a.sinks)) continue;
@@ -137,25 +157,65 @@ __global__ __launch_bounds__(NW * 64, NW > 2 ? 2 : 1) void attn_fwd_kernel(const
         read_ahead<4 * MT, 2, 4>();
     }
 
-    if (r >= a.rows) return;
     l = half_sum(l);
-    const int i = a.by_group.div(r), g = r - i * a.G;
-    const bool there = r < r_end;
-    if (a.nsplit > 1) {
-        const int64_t at = ((int64_t)split * a.B * a.Hkv + bh) * a.rows + r;
-        float* part = a.part + at * (a.D + 2);
+    float top2 = m == -INFINITY ? -INFINITY : mc - kLift;  // the reference that l and o are relative to, in log2 units
+    // What this lane stores: 4 dimensions from mt * 32 + 8 * group + 4 * h on,
+    // for each mt and GROUPS groups from group0 on.
+    constexpr int GROUPS = APART ? 1 : 4;
+    const int group0 = APART ? wave : 0;
+    floatx4_t sum[MT][GROUPS];
+    if constexpr (APART) {
+        // Every wave's part of the 32 rows, through LDS: [wave][mt][group][lane].
+        sync_all();
+        const u32 part = lds + wave * (MT * 4096) + lane * 16, stat = lds + kWaves * MT * 4096 + (lane & 31) * 8;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int j = 0; j < 16; j += 2) {
-                const int d = mt * 32 + 8 * (j / 4) + 4 * h + j % 4;
-                floatx2_t w = {o[mt][j], o[mt][j + 1]};
-                if (d < a.D) *(floatx2_t*)(part + 2 + d) = w;
+            for (int g = 0; g < 4; ++g) {
+                const floatx4_t y = {o[mt][4 * g], o[mt][4 * g + 1], o[mt][4 * g + 2], o[mt][4 * g + 3]};
+                lds_write16(part + (mt * 4 + g) * 1024, __builtin_bit_cast(u32x4_t, y));
             }
-        if (h == 0) {
-            floatx2_t w = {m == -INFINITY ? -INFINITY : mc - kLift, l};
-            *(floatx2_t*)part = w;
+        if (h == 0) lds_write8(stat + wave * 256, floatx2_t{top2, l});
+        sync_all();
+        floatx2_t ml[kWaves];
+        float most = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            ml[w] = lds_read8(stat + w * 256);
+            most = fmaxf(most, ml[w][0]);
         }
+        top2 = most;
+        l = 0;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) sum[mt][0] = floatx4_t{0, 0, 0, 0};
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            const float f = ml[w][0] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml[w][0] - most);
+            l = fmaf(ml[w][1], f, l);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+                sum[mt][0] += f * __builtin_bit_cast(floatx4_t, lds_read16(lds + (w * MT + mt) * 4096 + group0 * 1024 + lane * 16));
+        }
+    } else {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) sum[mt][g] = floatx4_t{o[mt][4 * g], o[mt][4 * g + 1], o[mt][4 * g + 2], o[mt][4 * g + 3]};
+    }
+
+    if (r >= a.rows) return;
+    const bool states = h == 0 && (!APART || wave == 0);  // one lane of a row writes its statistics
+    const int i = a.by_group.div(r), g = r - i * a.G;
+    const bool there = r < r_end;
+    if (APART && a.nsplit > 1) {
+        const int64_t at = ((int64_t)split * a.B * a.Hkv + bh) * a.rows + r;
+        float* part = a.part + at * (a.D + 4);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            const int d = mt * 32 + 8 * group0 + 4 * h;
+            if (d < a.D) *(floatx4_t*)(part + 4 + d) = sum[mt][0];
+        }
+        if (states) *(floatx2_t*)part = floatx2_t{top2, l};
         return;
     }
     const float inv = there && l != 0 ? 1.0f / l : 0.0f;
@@ -163,16 +223,16 @@ __global__ __launch_bounds__(NW * 64, NW > 2 ? 2 : 1) void attn_fwd_kernel(const
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int j = 0; j < 16; j += 4) {
-            const int d = mt * 32 + 8 * (j / 4) + 4 * h;
-            u32x2_t w = {pack2<BF>(o[mt][j] * inv, o[mt][j + 1] * inv),
-                         pack2<BF>(o[mt][j + 2] * inv, o[mt][j + 3] * inv)};
+        for (int j = 0; j < GROUPS; ++j) {
+            const int d = mt * 32 + 8 * (group0 + j) + 4 * h;
+            const floatx4_t y = sum[mt][j];
+            u32x2_t w = {pack2<BF>(y[0] * inv, y[1] * inv), pack2<BF>(y[2] * inv, y[3] * inv)};
             if (!there) w = (u32x2_t)(0u);
             if (d < a.D) *(u32x2_t*)(out + d * 2) = w;
         }
-    if (a.lse && h == 0)
+    if (a.lse && states)
         a.lse[((int64_t)b * a.Hq + hk * a.G + g) * a.Lq + i] =
-            there && l != 0 ? (mc - kLift + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+            there && l != 0 ? (top2 + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
 }
 
 // Joins the splits of a row: out = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s.
@@ -189,8 +249,8 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnParams a)
     const int b = bh / a.Hkv, hk = bh % a.Hkv, i = a.by_group.div(r), g = r - i * a.G;
     const Span s(a, b);
     const bool on = row < all && i < s.nq;
-    const float* part = a.part + row * (a.D + 2);
-    const int64_t step = all * (a.D + 2);
+    const float* part = a.part + row * (a.D + 4);
+    const int64_t step = all * (a.D + 4);
     float m = -INFINITY, l = 0;
     floatx4_t o = {0, 0, 0, 0};
     const auto add = [&](float m1, float l1, floatx4_t o1) {
@@ -205,12 +265,8 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnParams a)
         for (int j = group % P; j < a.nsplit; j += P) {
             const float* x = part + j * step;
             const floatx2_t ml = *(const floatx2_t*)x;
-            floatx2_t lo = {0, 0}, hi = {0, 0};
-            if (d < a.D) {
-                lo = *(const floatx2_t*)(x + 2 + d);
-                hi = *(const floatx2_t*)(x + 4 + d);
-            }
-            const floatx4_t o1 = {lo[0], lo[1], hi[0], hi[1]};
+            floatx4_t o1 = {0, 0, 0, 0};
+            if (d < a.D) o1 = *(const floatx4_t*)(x + 4 + d);
             if (ml[0] != -INFINITY) add(ml[0], ml[1], o1);
         }
     }
@@ -236,34 +292,34 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnParams a)
             l != 0 ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
 }
 
-template <bool BF, int NW>
+template <bool BF, int ROWS>
 int run(const AttnParams& a, hipStream_t st)
 {
     const unsigned grid = (unsigned)((int64_t)a.B * a.Hkv * a.tiles * a.nsplit);
     return with_head(a.D, [&](auto DP) {
-        if (a.table) attn_fwd_kernel<BF, DP.value, NW, true><<<grid, NW * 64, 0, st>>>(a);
-        else attn_fwd_kernel<BF, DP.value, NW, false><<<grid, NW * 64, 0, st>>>(a);
+        if (a.table) attn_fwd_kernel<BF, DP.value, ROWS, true><<<grid, kWaves * 64, 0, st>>>(a);
+        else attn_fwd_kernel<BF, DP.value, ROWS, false><<<grid, kWaves * 64, 0, st>>>(a);
         return launch_status();
     });
 }
 
 }  // namespace
 
-// Tiles of 128 rows where they fill the card's 256 CUs, else of 32; where even
+// Tiles of 128 rows where they fill the card's 256 CUs, else of 32. Where even
 // those leave it idle and walk more than 4 key tiles, the keys are split until
-// 512 workgroups are there or a workgroup is down to one key tile. (A short
-// walk ends before a second launch would join its parts.)
+// 256 workgroups are there or a workgroup is down to two tiles. (A wave's only
+// tile ends before a second launch would join parts of the walk.)
 AttnPlan attn_plan(const AttnParams& a)
 {
     AttnPlan p{};
     const int64_t heads = (int64_t)a.B * a.Hkv;
-    p.waves = heads * ceil_div(a.rows, 128) >= 256 ? 4 : 1;
-    p.tiles = ceil_div(a.rows, p.waves * 32);
+    p.tile_rows = heads * ceil_div(a.rows, 128) >= 256 ? 128 : 32;
+    p.tiles = ceil_div(a.rows, p.tile_rows);
     const int64_t groups = heads * p.tiles;
-    const int64_t keys = std::min<int64_t>((int64_t)a.window + p.waves * 32 / a.G, a.Lk) + std::min(a.sinks, a.Lk);
+    const int64_t keys = std::min<int64_t>((int64_t)a.window + p.tile_rows / a.G, a.Lk) + std::min(a.sinks, a.Lk);
     const int64_t most = std::max<int64_t>(1, (keys + kKeyTile - 1) / kKeyTile);
-    p.nsplit = p.waves == 4 || most <= 4 ? 1 : (int)std::min<int64_t>(most, (512 + groups - 1) / groups);
-    p.ws_bytes = p.nsplit > 1 ? (size_t)p.nsplit * heads * a.rows * (a.D + 2) * 4 : 0;
+    p.nsplit = p.tile_rows == 128 || most <= kWaves ? 1 : (int)std::min<int64_t>((most + 1) / 2, (256 + groups - 1) / groups);
+    p.ws_bytes = p.nsplit > 1 ? (size_t)p.nsplit * heads * a.rows * (a.D + 4) * 4 : 0;
     return p;
 }
 
@@ -272,8 +328,8 @@ int launch_attn_fwd(AttnParams a, const AttnPlan& plan, bool bf, hipStream_t st)
     a.tiles = plan.tiles;
     a.nsplit = plan.nsplit;
     int rc;
-    if (plan.waves == 4) rc = bf ? run<true, 4>(a, st) : run<false, 4>(a, st);
-    else rc = bf ? run<true, 1>(a, st) : run<false, 1>(a, st);
+    if (plan.tile_rows == 128) rc = bf ? run<true, 128>(a, st) : run<false, 128>(a, st);
+    else rc = bf ? run<true, 32>(a, st) : run<false, 32>(a, st);
     if (rc != 0 || a.nsplit == 1) return rc;
     const int64_t all = (int64_t)a.B * a.Hkv * a.rows;
     if (a.nsplit < 8) {

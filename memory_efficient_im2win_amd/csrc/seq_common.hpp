@@ -115,6 +115,10 @@ __device__ __forceinline__ void sync_but()
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
+// A wave that shares its LDS with no other: its copies have arrived; its reads are done.
+__device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ void wait_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
 // Elements of an LDS row for a head size padded to DP.
 __host__ __device__ constexpr int row_pitch(int DP) { return DP <= 64 ? 64 : 128; }
 
@@ -135,6 +139,16 @@ __device__ __forceinline__ u32x4_t lds_read16(u32 at)
 __device__ __forceinline__ void lds_write16(u32 at, u32x4_t v)
 {
     *(__attribute__((address_space(3))) u32x4_t*)(uintptr_t)at = v;
+}
+
+__device__ __forceinline__ floatx2_t lds_read8(u32 at)
+{
+    return *(__attribute__((address_space(3))) const floatx2_t*)(uintptr_t)at;
+}
+
+__device__ __forceinline__ void lds_write8(u32 at, floatx2_t v)
+{
+    *(__attribute__((address_space(3))) floatx2_t*)(uintptr_t)at = v;
 }
 
 // Reading operands. A reader holds one address; every other one of a tile is

@@ -45,7 +45,7 @@ struct AttnParams {
 
 // How a forward call is laid out.
 struct AttnPlan {
-    int waves, tiles, nsplit;
+    int tile_rows, tiles, nsplit;
     size_t ws_bytes;
 };
 AttnPlan attn_plan(const AttnParams& a);
