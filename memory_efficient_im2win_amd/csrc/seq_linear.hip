@@ -20,9 +20,12 @@
 //
 // Roundings to the element type: the chunk's decayed products q k^T, the state
 // as q's operand, and v times its decay. The first two enter only `out`,
-// which is rounded to the same type. Decayed values enter the state, so they
-// are split into a sum of parts of the type (bf16: 3 parts, 24 bits; fp16: 2,
-// 22 bits) where the caller asks for the last state; else they are rounded too.
+// which is rounded to the same type. (Two parts each, as a sum of two roundings,
+// took the outputs of a long prompt from 118 to 132 us.) Decayed values enter
+// the state, so they are split into a sum of parts of the type: bf16 3 parts, 24
+// bits, fp16 2, 22 bits, where the caller asks for the last state; two where the
+// state only leads to outputs (118 us against 116 with one); one for dk and dv
+// side by side, where two took 109 + 56 us and one takes 95 + 43.
 #include "seq_common.hpp"
 #include "seq_kernels.hpp"
 
@@ -39,43 +42,53 @@ constexpr bool has_outputs(int mode) { return mode >= kOutputs; }
 __device__ __forceinline__ int walk(int t, int n, bool reverse) { return reverse && t < n ? n - 1 - t : t; }
 
 // Copies 32 tokens of a tensor (x: its first token of the head) from walk
-// position t0 into the LDS tile. Chunks past the head size are not written:
-// they are zeroed once.
+// position t0 into an LDS tile, by NW waves. Chunks past the head size are not
+// written: they are zeroed once.
 template <int LP, int NW>
-__device__ __forceinline__ void stage_tokens(const unsigned char* x, int64_t sl, int d, int t0, int n, bool reverse,
-                                             u32 lds)
-{
-    constexpr int CH = LP / 8, RPI = 64 / CH, N = kChunk / RPI;
-    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    const bool whole = t0 + kChunk <= n;
-    // The tile's token with the lowest address, and the lane's row from there.
-    const unsigned char* first = x + (reverse ? n - t0 - kChunk : t0) * sl;
+struct TokenStage {
+    static constexpr int CH = LP / 8, RPI = 64 / CH, N = kChunk / RPI, J = (N + NW - 1) / NW;
+    const unsigned char* x;
+    int64_t sl;
+    int d, n, wave, lane;
+    bool reverse;
+    u32 at[J];  // byte offsets from the tile's token with the lowest address
+
+    __device__ __forceinline__ TokenStage(const unsigned char* x_, int64_t sl_, int d_, int n_, bool reverse_)
+        : x(x_), sl(sl_), d(d_), n(n_), wave(uniform(threadIdx.x >> 6)), lane(threadIdx.x & 63), reverse(reverse_)
+    {
 #pragma unroll
-    for (int j = 0; j < (N + NW - 1) / NW; ++j) {
-        const int part = j * NW + wave;
-        if (N % NW != 0 && part >= N) break;
-        const u32 row = part * RPI + lane / CH;
-        const u32 c = (lane % CH) ^ swz<LP>(row);
-        if ((int)c * 8 >= d) continue;
-        if (whole) {
-            dma16(first, (reverse ? kChunk - 1 - row : row) * (u32)sl + c * 16, lds + part * 1024);
-        } else {
-            const int t = t0 + (int)row;
-            dma16(t < n ? x + walk(t, n, reverse) * sl + c * 16 : (const unsigned char*)kAbsent.zero,
-                  lds + part * 1024);
+        for (int j = 0; j < J; ++j) at[j] = (reverse ? kChunk - 1 - row(j) : row(j)) * (u32)sl + chunk(j) * 16;
+    }
+    __device__ __forceinline__ u32 row(int j) const { return (j * NW + wave) * RPI + lane / CH; }
+    __device__ __forceinline__ u32 chunk(int j) const { return (lane % CH) ^ swz<LP>(row(j)); }
+    // WHOLE: all 32 tokens are there; FULL: the head size is LP.
+    template <bool WHOLE, bool FULL>
+    __device__ __forceinline__ void copy(int t0, u32 lds) const
+    {
+        const unsigned char* first = x + (reverse ? n - t0 - kChunk : t0) * sl;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int part = j * NW + wave;
+            if (N % NW != 0 && part >= N) break;
+            if (!FULL && (int)chunk(j) * 8 >= d) continue;
+            if (WHOLE) {
+                dma16(first, at[j], lds + part * 1024);
+            } else {
+                const int t = t0 + (int)row(j);
+                dma16(t < n ? x + walk(t, n, reverse) * sl + chunk(j) * 16 : (const unsigned char*)kAbsent.zero,
+                      lds + part * 1024);
+            }
         }
     }
-}
+};
 
-// x times w in parts of the element type that sum to it.
-template <bool BF, int PARTS>
-__device__ __forceinline__ void split_parts(u32x4_t x, const float* w, u32x4_t* out)
+// 8 floats, given by number, in parts of the element type that sum to them.
+template <bool BF, int PARTS, typename F>
+__device__ __forceinline__ void split_floats(F x, u32x4_t* out)
 {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        floatx2_t f = unpack2<BF>(x[j]);
-        f[0] *= w[2 * j];
-        f[1] *= w[2 * j + 1];
+        floatx2_t f = {x(2 * j), x(2 * j + 1)};
 #pragma unroll
         for (int p = 0; p < PARTS; ++p) {
             const u32 r = pack2<BF>(f[0], f[1]);
@@ -100,8 +113,11 @@ __global__ __launch_bounds__(DVP * (PAIR ? 4 : 2), 2) void linear_kernel(const L
     constexpr int LK = row_pitch(DKP), LV = row_pitch(DVP), KS = DKP / 16, MT = DKP / 32;
     constexpr int TK = kChunk * LK * 2, TV = kChunk * LV * 2, OUT = has_outputs(MODE);
     constexpr int BUF = TK + TV + OUT * (PAIR ? 2 : 1) * TK;  // k, v, q (and the second job's q)
-    constexpr int PARTS = MODE == kOutputs || MODE == kRoughStates ? 1 : BF ? 3 : 2;
-    __shared__ __align__(1024) unsigned char smem[2 * BUF];
+    constexpr int PARTS = MODE == kOutputs || MODE == kRoughStates ? (PAIR ? 1 : 2) : BF ? 3 : 2;
+    // Chunks under way beside the one at hand, and the fewest copies a wave issues for one.
+    constexpr int AHEAD = OUT && !PAIR ? 2 : 3, BUFS = AHEAD + 1;
+    constexpr int COPIES = (LK / 16) / ALL * (OUT ? PAIR ? 3 : 2 : 1) + (LV / 16) / ALL;
+    __shared__ __align__(1024) unsigned char smem[BUFS * BUF];
     const u32 lds = (u32)(uintptr_t)(lds_byte*)smem;
     const int lane = threadIdx.x & 63, h = lane >> 5, col = lane & 31;
     const int role = PAIR ? uniform(threadIdx.x >> 6) / NW : 0;
@@ -126,21 +142,29 @@ __global__ __launch_bounds__(DVP * (PAIR ? 4 : 2), 2) void linear_kernel(const L
     }
 
     const auto head = [&](const Tensor& x) { return x.p + b * x.sb + hd * x.sh; };
-    const unsigned char *const xk = head(J0.k), *const xv = head(J0.v), *const xq = head(J0.q);
-    const unsigned char* const xq1 = PAIR ? head(a.job[1].q) : nullptr;
-    const int64_t slk = J0.k.sl, slv = J0.v.sl, slq = J0.q.sl, slq1 = PAIR ? a.job[1].q.sl : 0;
-    const int dk0 = J0.dk, dv0 = J0.dv;
+    const TokenStage<LK, ALL> to_k(head(J0.k), J0.k.sl, J0.dk, n, reverse);
+    const TokenStage<LV, ALL> to_v(head(J0.v), J0.v.sl, J0.dv, n, reverse);
+    const TokenStage<LK, ALL> to_q(head(J0.q), J0.q.sl, J0.dk, n, reverse);
+    const TokenStage<LK, ALL> to_q1(PAIR ? head(a.job[1].q) : nullptr, PAIR ? a.job[1].q.sl : 0, J0.dv, n, reverse);
+    const auto copy = [&](int t, u32 at, auto whole, auto full) {
+        to_k.template copy<whole.value, full.value>(t, at);
+        to_v.template copy<whole.value, full.value>(t, at + TK);
+        if (OUT) to_q.template copy<whole.value, full.value>(t, at + TK + TV);
+        if (OUT && PAIR) to_q1.template copy<whole.value, full.value>(t, at + TK + TV + TK);
+    };
+    const bool full = J0.dk == LK && J0.dv == LV;
     const auto stage = [&](int t, u32 at) {
-        stage_tokens<LK, ALL>(xk, slk, dk0, t, n, reverse, at);
-        stage_tokens<LV, ALL>(xv, slv, dv0, t, n, reverse, at + TK);
-        if (OUT) stage_tokens<LK, ALL>(xq, slq, dk0, t, n, reverse, at + TK + TV);
-        if (OUT && PAIR) stage_tokens<LK, ALL>(xq1, slq1, dv0, t, n, reverse, at + TK + TV + TK);
+        if (t + kChunk > n) copy(t, at, std::false_type{}, std::false_type{});
+        else if (full) copy(t, at, std::true_type{}, std::true_type{});
+        else copy(t, at, std::true_type{}, std::false_type{});
     };
     if (J.dk != LK || J.dv != LV) {
-        for (int at = threadIdx.x * 16; at < 2 * BUF; at += ALL * 1024) lds_write16(lds + at, u32x4_t{});
+        for (int at = threadIdx.x * 16; at < BUFS * BUF; at += ALL * 1024) lds_write16(lds + at, u32x4_t{});
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     }
-    if (t_begin < t_live) stage(t_begin, lds);
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+        if (t_begin + i * kChunk < t_live) stage(t_begin + i * kChunk, lds + i * BUF);
 
     // The state: from the workspace in register order, or the one given.
     floatx16_t S[MT] = {};
@@ -183,15 +207,31 @@ __global__ __launch_bounds__(DVP * (PAIR ? 4 : 2), 2) void linear_kernel(const L
     };
     set_to_end(kChunk);
 
+    // A chunk's outputs are stored a turn later, before that turn's copies: the
+    // youngest loads are then always copies, and the wait for a chunk leaves them under way.
+    u32x4_t held[2];
+    const auto store = [&](int t0) {
+        if (t0 + col >= t_end) return;
+        const bool there = t0 + col < n;
+        unsigned char* out = J.out.p + b * J.out.sb + walk(t0 + col, n, reverse) * J.out.sl + hd * J.out.sh;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int d = wave * 32 + 16 * i + 8 * h;
+            if (d < J.dv) *(u32x4_t*)(out + d * 2) = there ? held[i] : u32x4_t{};
+        }
+    };
+
     settle_loads();
 
     int t = t_begin;
-    for (int it = 0; t < t_live; t += kChunk, ++it) {
-        const u32 buf = lds + (it & 1) * BUF;
+    u32 buf = lds, next = lds + AHEAD * BUF;
+    for (; t < t_live; t += kChunk) {
         const u32 kt = buf + (role ? TK : 0), vt = buf + (role ? 0 : TK), qt = buf + TK + TV + (role ? TK : 0);
         const int tokens = min(kChunk, t_live - t);
-        sync_all();
-        if (t + kChunk < t_live) stage(t + kChunk, lds + ((it + 1) & 1) * BUF);
+        if (t + (AHEAD - 1) * kChunk < t_live) sync_but<COPIES*(AHEAD - 1)>();
+        else sync_all();
+        if (OUT && t > t_begin) store(t - kChunk);
+        if (t + AHEAD * kChunk < t_live) stage(t + AHEAD * kChunk, next);
         if (tokens < kChunk) set_to_end(tokens);
 
         const RowsOf<LK> kr(kt, col), qr(qt, col);
@@ -211,9 +251,7 @@ __global__ __launch_bounds__(DVP * (PAIR ? 4 : 2), 2) void linear_kernel(const L
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
                 u32x4_t sp;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    sp[j] = pack2<BF>(S[ks / 2][(ks % 2) * 8 + 2 * j], S[ks / 2][(ks % 2) * 8 + 2 * j + 1]);
+                split_floats<BF, 1>([&](int j) { return S[ks / 2][(ks % 2) * 8 + j]; }, &sp);
                 o = mfma<BF>(sp, q[ks], o);
             }
             // The first operands, then a product, the reads of a later one and
@@ -228,24 +266,22 @@ __global__ __launch_bounds__(DVP * (PAIR ? 4 : 2), 2) void linear_kernel(const L
             o *= from_start;
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                u32x4_t p;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    p[j] = pack2<BF>(sc[8 * s + 2 * j] * between[8 * s + 2 * j],
-                                     sc[8 * s + 2 * j + 1] * between[8 * s + 2 * j + 1]);
-                o = mfma<BF>(v[s], p, o);
+                u32x4_t x;
+                split_floats<BF, 1>([&](int j) { return sc[8 * s + j] * between[8 * s + j]; }, &x);
+                o = mfma<BF>(v[s], x, o);
             }
-            if (t + col < t_end) {
-                const bool there = t + col < n;
-                unsigned char* out = J.out.p + b * J.out.sb + walk(t + col, n, reverse) * J.out.sl + hd * J.out.sh;
+            // Registers 8i .. 8i+7: 4 columns in each half, then the next 4;
+            // exchanged between the halves, 8 neighbouring columns a lane.
 #pragma unroll
-                for (int i = 0; i < 16; i += 4) {
-                    const int d = wave * 32 + 8 * (i / 4) + 4 * h;
-                    u32x2_t w = {pack2<BF>(o[i], o[i + 1]), pack2<BF>(o[i + 2], o[i + 3])};
-                    if (!there) w = (u32x2_t)(0u);
-                    if (d < J.dv) *(u32x2_t*)(out + d * 2) = w;
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const auto x = __builtin_amdgcn_permlane32_swap(pack2<BF>(o[8 * i + 2 * j], o[8 * i + 2 * j + 1]),
+                                                                    pack2<BF>(o[8 * i + 4 + 2 * j], o[8 * i + 5 + 2 * j]),
+                                                                    false, false);
+                    held[i][j] = x[0];
+                    held[i][2 + j] = x[1];
                 }
-            }
         }
         const float fall = __builtin_amdgcn_exp2f(g * (float)tokens);
 #pragma unroll
@@ -253,7 +289,7 @@ __global__ __launch_bounds__(DVP * (PAIR ? 4 : 2), 2) void linear_kernel(const L
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             u32x4_t w[PARTS];
-            split_parts<BF, PARTS>(v[s], to_end[s], w);
+            split_floats<BF, PARTS>([&](int j) { return unpack2<BF>(v[s][j / 2])[j % 2] * to_end[s][j]; }, w);
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
                 const u32x4_t k = kc.get(s * 16, mt);
@@ -261,9 +297,13 @@ __global__ __launch_bounds__(DVP * (PAIR ? 4 : 2), 2) void linear_kernel(const L
                 for (int p = 0; p < PARTS; ++p) S[mt] = mfma<BF>(k, w[p], S[mt]);
             }
         }
+        buf = buf == lds + AHEAD * BUF ? lds : buf + BUF;
+        next = next == lds + AHEAD * BUF ? lds : next + BUF;
     }
 
-    if (OUT) {  // tokens past the sequence
+    if (OUT) {
+        if (t > t_begin) store(t - kChunk);
+        // Tokens past the sequence.
         const int first = max(t, t_begin);
         for (int at = first + wave; at < t_end; at += NW) {
             unsigned char* out = J.out.p + b * J.out.sb + at * J.out.sl + hd * J.out.sh;
