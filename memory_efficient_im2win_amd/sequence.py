@@ -34,117 +34,142 @@ __all__ = ["window_attention", "window_attention_backward", "window_attention_wo
 # seq_attention and seq_linear of include/im2win_seq.h.
 _ATTENTION = struct.Struct("<16q5q11if16q")
 _LINEAR = struct.Struct("<16q4q6if4x16q2q")
-_NONE = (0, 0, 0, 0)
-_NO_GRADS = _NONE * 4
-_NO_TAIL = _NO_GRADS + (0, 0)
-_torch = _raw_stream = None
+# The same with a tensor's strides, and what else a plan holds, packed before:
+# a call fills in pointers. (Packing every field took 0.9 us of a call, this 0.3.)
+_STRIDES = struct.Struct("<3q")
+_ATTENTION_FORWARD = struct.Struct("<" + "q24s" * 4 + "4q56s128x")
+_ATTENTION_BACKWARD = struct.Struct("<" + "q24s" * 4 + "4q56s" + "q24s" * 4)
+_ATTENTION_SIZES = struct.Struct("<q11if")
+_LINEAR_FORWARD = struct.Struct("<" + "q24s" * 4 + "4q32s144x")
+_LINEAR_BACKWARD = struct.Struct("<" + "q24s" * 3 + "32x4q32s" + "q24s" * 4 + "2q")
+_LINEAR_SIZES = struct.Struct("<6if4x")
+_torch = _raw_stream = _lib_handle = _contiguous = None
+_CODES = {}
 
 
-def _dtype_code(t):
-    global _torch, _raw_stream
-    if _torch is None:
-        import torch
-        # torch.cuda.current_stream(device).cuda_stream without the object in
-        # between, which costs as much as the rest of a call's checks.
-        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-            (lambda index: torch.cuda.current_stream(index).cuda_stream)
-        _torch = torch
-    dtype = t.dtype
-    if dtype is _torch.bfloat16:
-        return 1
-    if dtype is _torch.float16:
-        return 0
-    raise TypeError(f"expected float16 or bfloat16 tensors, got {dtype}")
+def _setup():
+    global _torch, _raw_stream, _lib_handle, _contiguous
+    import torch
+    # torch.cuda.current_stream(device).cuda_stream without the object in
+    # between, which costs as much as the rest of a call's checks.
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _contiguous = torch.contiguous_format
+    _CODES.update({torch.float16: 0, torch.bfloat16: 1})
+    _lib_handle = _lib.load()
+    _torch = torch
 
 
-def _tensor(t, name, like, shape):
-    """(pointer, batch, token and head stride) of a 16-bit tensor (batch,
-    token, head, size), or (batch, head, size) of single tokens."""
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    if t.dtype is not like.dtype:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected {like.dtype}")
-    if t.device != like.device:
-        raise ValueError(f"{name} must be on {like.device}")
+@functools.lru_cache(maxsize=1024)
+def _strides(name, shape, stride, expected):
+    """The packed batch, token and head stride of a 16-bit tensor (batch, token,
+    head, size), or (batch, head, size) of single tokens."""
+    if shape != expected:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected {tuple(expected)}")
     if len(shape) == 4:
-        sb, sl, sh, sd = t.stride()
+        sb, sl, sh, sd = stride
         B, L, H, _ = shape
-        if L <= 1:
-            sl = 0
-            if L == 0:
-                return _NONE
     else:
-        sb, sh, sd = t.stride()
+        sb, sh, sd = stride
         B, H, _ = shape
-        sl = 0
+        sl, L = 0, 1
+    if B == 0 or L == 0:
+        return _STRIDES.pack(0, 0, 0)
     # The stride of an extent of one means nothing.
-    if B <= 1:
-        sb = 0
-        if B == 0:
-            return _NONE
-    if H == 1:
-        sh = 0
+    sb, sl, sh = sb if B > 1 else 0, sl if L > 1 else 0, sh if H > 1 else 0
+    if sd != 1 or (sb | sl | sh) & 7 or sl >= 1 << 24:
+        raise _unfit(name)
+    return _STRIDES.pack(sb, sl, sh)
+
+
+def _unfit(name):
+    return ValueError(f"{name} needs an innermost stride of 1, other strides that are multiples of 8 elements "
+                      "(from token to token below 2**24) and a 16-byte aligned start")
+
+
+@functools.lru_cache(maxsize=1024)
+def _dense(shape):
+    """The packed strides of a new tensor."""
+    head = shape[-1] * shape[-2]
+    return _STRIDES.pack(head * (shape[1] if len(shape) == 4 else 1), head if len(shape) == 4 else 0, shape[-1])
+
+
+def _gpu(t, name, dims):
+    """The index of t's device."""
+    if _torch is None:
+        _setup()
+    dev = t.get_device()
+    if dev < 0 or not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions")
+    return dev
+
+
+def _pointer(t, name, dtype, dev):
+    """The pointer of a 16-bit tensor whose shape and strides a plan has checked."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}")
     p = t.data_ptr()
-    if sd != 1 or (sb | sl | sh) & 7 or p & 15 or sl >= 1 << 24:
-        raise ValueError(f"{name} needs an innermost stride of 1, other strides that are multiples of 8 elements "
-                         "(from token to token below 2**24) and a 16-byte aligned start")
-    return p, sb, sl, sh
+    if p & 15 and t.numel():
+        raise _unfit(name)
+    return p
 
 
-def _output(t, name, like, shape):
-    """The output tensor given, or a new one, and its pointer and strides."""
+def _output(t, name, like, dev):
+    """The output tensor given, or a new one, of like's shape and type; its
+    pointer and packed strides."""
+    shape = like.shape
     if t is None:
-        t = _torch.empty(shape, dtype=like.dtype, device=like.device)
-        if len(shape) == 3:
-            return t, (t.data_ptr(), shape[1] * shape[2], 0, shape[2])
-        head = shape[2] * shape[3]
-        return t, (t.data_ptr(), shape[1] * head, head, shape[3])
-    r = _tensor(t, name, like, shape)
+        t = _torch.empty_like(like, memory_format=_contiguous)
+        return t, t.data_ptr(), _dense(shape)
+    b = _strides(name, t.shape, t.stride(), shape)
     if t.numel() and 0 in [s for s, n in zip(t.stride(), shape) if n > 1]:
         raise ValueError(f"{name} must not overlap itself")
-    return t, r
+    return t, _pointer(t, name, like.dtype, dev), b
 
 
-def _ints(t, name, like, shape, contiguous=True):
+def _ints(t, name, dev, shape, contiguous=True):
     if t is None:
         return 0
-    if t.dtype is not _torch.int32 or tuple(t.shape) != shape or t.device != like.device:
-        raise ValueError(f"{name} must be an int32 tensor of shape {shape} on {like.device}")
-    if t.numel() and (not t.is_contiguous() if contiguous else t.stride(-1) != 1 and t.shape[-1] > 1):
+    if t.dtype is not _torch.int32 or t.shape != shape or t.get_device() != dev:
+        raise ValueError(f"{name} must be an int32 tensor of shape {tuple(shape)} on cuda:{dev}")
+    if not t.is_contiguous() and t.numel() and (contiguous or t.stride(-1) != 1 and t.shape[-1] > 1):
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
-def _floats(t, name, like, shape):
+def _floats(t, name, dev, shape):
     if t is None:
         return 0
-    if t.dtype is not _torch.float32 or tuple(t.shape) != shape or t.device != like.device:
-        raise ValueError(f"{name} must be a float32 tensor of shape {shape} on {like.device}")
-    if not t.is_contiguous() or (t.dim() == 4 and t.data_ptr() & 15):
+    if t.dtype is not _torch.float32 or t.shape != shape or t.get_device() != dev:
+        raise ValueError(f"{name} must be a float32 tensor of shape {tuple(shape)} on cuda:{dev}")
+    p = t.data_ptr()
+    if not t.is_contiguous() or (len(shape) == 4 and p & 15):
         raise ValueError(f"{name} must be contiguous with a 16-byte aligned start")
-    return t.data_ptr()
+    return p
 
 
-def _call(name, args, like, ws, need):
-    """Runs entry point `name` with `need` bytes of scratch (None: it takes
-    none) on like's device."""
-    device = like.device
+def _call(fn, name, args, like, dev, ws, need):
+    """Runs entry point fn (`name`) with `need` bytes of scratch (None: it takes
+    none) on device dev."""
     ptr, size = 0, 0
     if ws is not None:
-        if not ws.is_cuda or not ws.is_contiguous() or ws.device != device:
-            raise ValueError(f"ws must be a contiguous GPU tensor on {device}")
+        if not ws.is_cuda or not ws.is_contiguous() or ws.get_device() != dev:
+            raise ValueError(f"ws must be a contiguous GPU tensor on cuda:{dev}")
         if need:
             ptr, size = ws.data_ptr(), ws.numel() * ws.element_size()
     elif need:
-        ws = _torch.empty(need, dtype=_torch.uint8, device=device)
+        ws = like.new_empty((need + 1) // 2)
         ptr, size = ws.data_ptr(), need
-    stream = _raw_stream(device.index)
+    stream = _raw_stream(dev)
     args = (args, stream) if need is None else (args, ptr, size, stream)
-    fn = getattr(_lib.load(), name)
-    if device.index == _torch.cuda.current_device():
+    if dev == _torch.cuda.current_device():
         status = fn(*args)
     else:
-        with _torch.cuda.device(device):
+        with _torch.cuda.device(dev):
             status = fn(*args)
     if status:
         _lib.check(status, name)
@@ -165,59 +190,66 @@ def _linear_bytes(B, L, H, Dk, Dv, backward):
     return (lib.im2win_seq_linear_backward_workspace_bytes if backward else lib.im2win_seq_linear_workspace_bytes)(args)
 
 
-def _gpu(t, name, dims=4):
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a GPU tensor")
-    if t.dim() != dims:
-        raise ValueError(f"{name} must have {dims} dimensions")
-    return _dtype_code(t)
+def _scale(scale, D):
+    if scale is None:
+        scale = D ** -0.5
+    if scale - scale != 0:
+        raise ValueError("scale must be finite")
+    return scale
 
 
-def _attention_args(q, k, v, window, sinks, scale, q_lens, kv_lens, page_table):
-    """The packed argument up to the outputs, a function of (out, lse, grads),
-    the shapes of q and of k and v, and the sizes that scratch memory goes by."""
-    code = _gpu(q, "q")
-    if k.dim() != 4:
+def _code(dtype):
+    if dtype not in _CODES:
+        raise TypeError(f"expected float16 or bfloat16 tensors, got {dtype}")
+    return _CODES[dtype]
+
+
+# What follows from the shapes, strides and numbers of a call alone: checked and
+# packed once for each combination (5 of the 12 us that a call took).
+@functools.lru_cache(maxsize=1024)
+def _attention_plan(dtype, q, q_stride, k, k_stride, v, v_stride, table, table_stride, window, sinks, scale):
+    """(strides of q, k and v; q's shape; sizes, packed, and as scratch
+    memory goes by them)"""
+    code = _code(dtype)
+    if len(k) != 4:
         raise ValueError("k must have 4 dimensions")
-    B, Lq, Hq, D = q.shape
-    Hkv = k.shape[2]
-    page = pages = table = table_stride = 0
-    if page_table is None:
-        Lk = k.shape[1]
+    B, Lq, Hq, D = q
+    Hkv = k[2]
+    page = pages = step = 0
+    if table is None:
+        Lk = k[1]
         kv_shape = (B, Lk, Hkv, D)
     else:
-        pages, page = k.shape[0], k.shape[1]
-        if page_table.dim() != 2:
+        pages, page = k[:2]
+        if len(table) != 2:
             raise ValueError("page_table must have 2 dimensions")
-        per = page_table.shape[1]
-        table = _ints(page_table, "page_table", q, (B, per), contiguous=False)
-        table_stride, Lk = page_table.stride(0), per * page
         kv_shape = (pages, page, Hkv, D)
+        step, Lk = table_stride[0], table[1] * page
         if page < 1:
             raise ValueError("a page must hold a token")
-        if table == 0:  # no pages at all: nothing is there to see
-            page = pages = Lk = 0
+        if table[0] != B:
+            raise ValueError(f"page_table must have {B} rows")
+        if Lk == 0 or B == 0:  # no pages at all: nothing is there to see
+            page = pages = step = Lk = 0
     if Hkv < 1 or Hq < 1 or Hq % Hkv:
         raise ValueError(f"{Hq} query heads cannot share {Hkv} key heads evenly")
     if D < 8 or D > 128 or D % 8:
         raise ValueError("the head size must be a multiple of 8 from 8 to 128")
-    window = max(Lk, 1) if window is None else int(window)
-    sinks = int(sinks)
+    if window is None:
+        window = max(Lk, 1)
     if window < 1 or sinks < 0:
         raise ValueError("window must be at least 1 and sinks at least 0")
-    scale = D ** -0.5 if scale is None else float(scale)
-    if scale - scale != 0:
-        raise ValueError("scale must be finite")
-    tq, tk, tv = _tensor(q, "q", q, (B, Lq, Hq, D)), _tensor(k, "k", q, kv_shape), _tensor(v, "v", q, kv_shape)
-    lens = _ints(q_lens, "q_lens", q, (B,)), _ints(kv_lens, "kv_lens", q, (B,))
-
+    scale = _scale(scale, D)
+    strides = (_strides("q", q, q_stride, (B, Lq, Hq, D)), _strides("k", k, k_stride, kv_shape),
+               _strides("v", v, v_stride, kv_shape))
     window, sinks = min(window, 2**31 - 1), min(sinks, 2**31 - 1)
+    sizes = (B, Lq, Lk, Hq, Hkv, D, window, sinks)
+    packed = _ATTENTION_SIZES.pack(step, code, B, Lq, Lk, Hq, Hkv, D, page, pages, window, sinks, scale)
+    return strides, q, packed, sizes
 
-    def pack(out, lse, grads=_NO_GRADS):
-        return _ATTENTION.pack(*tq, *tk, *tv, *out, lse, *lens, table, table_stride, code, B, Lq, Lk, Hq, Hkv, D,
-                               page, pages, window, sinks, scale, *grads)
 
-    return pack, (B, Lq, Hq, D), kv_shape, (B, Lq, Lk, Hq, Hkv, D, window, sinks)
+def _numbers(window, sinks, scale):
+    return None if window is None else int(window), int(sinks), None if scale is None else float(scale)
 
 
 def window_attention(q, k, v, *, window=None, sinks=0, scale=None, q_lens=None, kv_lens=None, page_table=None,
@@ -240,15 +272,29 @@ def window_attention(q, k, v, *, window=None, sinks=0, scale=None, q_lens=None, 
     pages may be gone. A page number outside the pool makes the outputs that
     need it NaN.
     """
-    pack, q_shape, _, sizes = _attention_args(q, k, v, window, sinks, scale, q_lens, kv_lens, page_table)
-    out, t = _output(out, "out", q, q_shape)
+    dev, dtype = _gpu(q, "q", 4), q.dtype
+    strides, q_shape, packed, sizes = _attention_plan(
+        dtype, q.shape, q.stride(), k.shape, k.stride(), v.shape, v.stride(),
+        *((None, None) if page_table is None else (page_table.shape, page_table.stride())),
+        *_numbers(window, sinks, scale))
+    pq, pk, pv = _pointer(q, "q", dtype, dev), _pointer(k, "k", dtype, dev), _pointer(v, "v", dtype, dev)
     B, Lq, Hq, _ = q_shape
+    table = 0
+    if page_table is not None:
+        table = _ints(page_table, "page_table", dev, page_table.shape, contiguous=False)
+        if sizes[2] == 0:
+            table = 0
+    lens = (B,)
+    ql = 0 if q_lens is None else _ints(q_lens, "q_lens", dev, lens)
+    kl = 0 if kv_lens is None else _ints(kv_lens, "kv_lens", dev, lens)
+    out, po, so = _output(out, "out", q, dev)
     p = 0
     if return_lse or lse is not None:
         if lse is None:
-            lse = _torch.empty((B, Hq, Lq), dtype=_torch.float32, device=q.device)
-        p = _floats(lse, "lse", q, (B, Hq, Lq))
-    _call("im2win_seq_attention", pack(t, p), q, ws, _attention_bytes(*sizes, False))
+            lse = q.new_empty((B, Hq, Lq), dtype=_torch.float32)
+        p = _floats(lse, "lse", dev, (B, Hq, Lq))
+    args = _ATTENTION_FORWARD.pack(pq, strides[0], pk, strides[1], pv, strides[2], po, so, p, ql, kl, table, packed)
+    _call(_lib_handle.im2win_seq_attention, "im2win_seq_attention", args, q, dev, ws, _attention_bytes(*sizes, False))
     return (out, lse) if return_lse else out
 
 
@@ -257,16 +303,25 @@ def window_attention_backward(dout, q, k, v, out, lse, *, window=None, sinks=0, 
     """(dq, dk, dv) of window_attention without pages, from the gradient of its
     output and the ``out`` and ``lse`` that it returned. What lies past a
     sequence's end gets zeros."""
-    pack, q_shape, kv_shape, sizes = _attention_args(q, k, v, window, sinks, scale, q_lens, kv_lens, None)
+    dev, dtype = _gpu(q, "q", 4), q.dtype
+    strides, q_shape, packed, sizes = _attention_plan(
+        dtype, q.shape, q.stride(), k.shape, k.stride(), v.shape, v.stride(), None, None,
+        *_numbers(window, sinks, scale))
+    pq, pk, pv = _pointer(q, "q", dtype, dev), _pointer(k, "k", dtype, dev), _pointer(v, "v", dtype, dev)
     B, Lq, Hq, _ = q_shape
-    tout, tdout = _tensor(out, "out", q, q_shape), _tensor(dout, "dout", q, q_shape)
+    so, sdo = _strides("out", out.shape, out.stride(), q_shape), _strides("dout", dout.shape, dout.stride(), q_shape)
+    po, pdo = _pointer(out, "out", dtype, dev), _pointer(dout, "dout", dtype, dev)
     if lse is None:
         raise ValueError("lse is needed: call window_attention with return_lse=True")
-    p = _floats(lse, "lse", q, (B, Hq, Lq))
-    dq, a = _output(dq, "dq", q, q_shape)
-    dk, b = _output(dk, "dk", q, kv_shape)
-    dv, c = _output(dv, "dv", q, kv_shape)
-    _call("im2win_seq_attention_backward", pack(tout, p, (*tdout, *a, *b, *c)), q, ws, _attention_bytes(*sizes, True))
+    p = _floats(lse, "lse", dev, (B, Hq, Lq))
+    lens = _ints(q_lens, "q_lens", dev, (B,)), _ints(kv_lens, "kv_lens", dev, (B,))
+    dq, pdq, sdq = _output(dq, "dq", q, dev)
+    dk, pdk, sdk = _output(dk, "dk", k, dev)
+    dv, pdv, sdv = _output(dv, "dv", v, dev)
+    args = _ATTENTION_BACKWARD.pack(pq, strides[0], pk, strides[1], pv, strides[2], po, so, p, *lens, 0, packed,
+                                    pdo, sdo, pdq, sdq, pdk, sdk, pdv, sdv)
+    _call(_lib_handle.im2win_seq_attention_backward, "im2win_seq_attention_backward", args, q, dev, ws,
+          _attention_bytes(*sizes, True))
     return dq, dk, dv
 
 
@@ -274,26 +329,37 @@ def window_attention_workspace_bytes(B, Lq, Lk, Hq, Hkv, D, window=None, sinks=0
     """Scratch bytes of window_attention, or of its backward call, for these
     sizes (Lk: the table's pages times their size for a paged cache)."""
     window = max(Lk, 1) if window is None else int(window)
-    return _attention_bytes(B, Lq, Lk, Hq, Hkv, D, window, sinks, bool(backward))
+    return _attention_bytes(B, Lq, Lk, Hq, Hkv, D, min(window, 2**31 - 1), min(int(sinks), 2**31 - 1), bool(backward))
 
 
-def _linear_sizes(q, k, v, log_decay, scale, dims):
-    code = _gpu(q, "q", dims)
-    if v.dim() != dims:
+@functools.lru_cache(maxsize=1024)
+def _linear_plan(dtype, q, q_stride, k, k_stride, v, v_stride, scale):
+    """(strides of q, k and v; shapes of out and a state; sizes, packed, and as
+    scratch memory goes by them); single tokens: 3 dimensions."""
+    code, dims = _code(dtype), len(q)
+    if len(v) != dims:
         raise ValueError(f"v must have {dims} dimensions")
-    H, Dk = q.shape[-2:]
-    Dv = v.shape[-1]
+    B, H, Dk = q[0], q[-2], q[-1]
+    L, Dv = q[1] if dims == 4 else 1, v[-1]
     for d in (Dk, Dv):
         if d < 8 or d > 128 or d % 8:
             raise ValueError("head sizes must be multiples of 8 from 8 to 128")
     if H < 1:
         raise ValueError("there must be a head")
-    scale = Dk ** -0.5 if scale is None else float(scale)
-    if scale - scale != 0:
-        raise ValueError("scale must be finite")
+    scale = _scale(scale, Dk)
+    out = (B, L, H, Dv) if dims == 4 else (B, H, Dv)
+    strides = _strides("q", q, q_stride, q), _strides("k", k, k_stride, q), _strides("v", v, v_stride, out)
+    return strides, out, (B, H, Dk, Dv), _LINEAR_SIZES.pack(code, B, L, H, Dk, Dv, scale), (B, L, H, Dk, Dv)
+
+
+def _linear_inputs(q, k, v, log_decay, scale, dims):
+    dev, dtype = _gpu(q, "q", dims), q.dtype
+    plan = _linear_plan(dtype, q.shape, q.stride(), k.shape, k.stride(), v.shape, v.stride(),
+                        None if scale is None else float(scale))
     if log_decay is None:
         raise ValueError("log_decay is needed")
-    return code, H, Dk, Dv, scale, _floats(log_decay, "log_decay", q, (H,))
+    decay = _floats(log_decay, "log_decay", dev, (plan[2][1],))
+    return dev, plan, decay, _pointer(q, "q", dtype, dev), _pointer(k, "k", dtype, dev), _pointer(v, "v", dtype, dev)
 
 
 def linear_attention(q, k, v, log_decay, *, state=None, scale=None, lens=None, out=None, state_out=None, ws=None):
@@ -309,32 +375,29 @@ def linear_attention(q, k, v, log_decay, *, state=None, scale=None, lens=None, o
     sequences' lengths, default L; out is 0 past them. ``scale`` defaults to
     Dk ** -0.5.
     """
-    code, H, Dk, Dv, scale, decay = _linear_sizes(q, k, v, log_decay, scale, 4)
-    B, L = q.shape[:2]
-    qk, vo, st = (B, L, H, Dk), (B, L, H, Dv), (B, H, Dk, Dv)
-    out, t = _output(out, "out", q, vo)
+    dev, plan, decay, pq, pk, pv = _linear_inputs(q, k, v, log_decay, scale, 4)
+    strides, _, st, packed, sizes = plan
+    out, po, so = _output(out, "out", v, dev)
+    before = _floats(state, "state", dev, st)
     if state_out is None:
-        state_out = _torch.empty(st, dtype=_torch.float32, device=q.device)
-    args = _LINEAR.pack(*_tensor(q, "q", q, qk), *_tensor(k, "k", q, qk), *_tensor(v, "v", q, vo), *t, decay,
-                        _floats(state, "state", q, st), _floats(state_out, "state_out", q, st),
-                        _ints(lens, "lens", q, (B,)), code, B, L, H, Dk, Dv, scale, *_NO_TAIL)
-    _call("im2win_seq_linear", args, q, ws, _linear_bytes(B, L, H, Dk, Dv, False))
+        state_out = q.new_empty(st, dtype=_torch.float32) if state is None else _torch.empty_like(state)
+    args = _LINEAR_FORWARD.pack(pq, strides[0], pk, strides[1], pv, strides[2], po, so, decay, before,
+                                _floats(state_out, "state_out", dev, st), _ints(lens, "lens", dev, st[:1]), packed)
+    _call(_lib_handle.im2win_seq_linear, "im2win_seq_linear", args, q, dev, ws, _linear_bytes(*sizes, False))
     return out, state_out
 
 
 def linear_attention_step(q, k, v, log_decay, state, *, scale=None, out=None):
     """One token of linear_attention: q, k (B, H, Dk), v (B, H, Dv); out (B, H,
     Dv). ``state``, float32 (B, H, Dk, Dv), is updated in place."""
-    code, H, Dk, Dv, scale, decay = _linear_sizes(q, k, v, log_decay, scale, 3)
-    B = q.shape[0]
+    dev, plan, decay, pq, pk, pv = _linear_inputs(q, k, v, log_decay, scale, 3)
     if state is None:
         raise ValueError("state is needed")
-    qk, vo = (B, H, Dk), (B, H, Dv)
-    out, t = _output(out, "out", q, vo)
-    s = _floats(state, "state", q, (B, H, Dk, Dv))
-    args = _LINEAR.pack(*_tensor(q, "q", q, qk), *_tensor(k, "k", q, qk), *_tensor(v, "v", q, vo), *t, decay, s, s, 0,
-                        code, B, 1, H, Dk, Dv, scale, *_NO_TAIL)
-    _call("im2win_seq_linear_step", args, q, None, None)
+    strides, _, st, packed, _ = plan
+    out, po, so = _output(out, "out", v, dev)
+    p = _floats(state, "state", dev, st)
+    args = _LINEAR_FORWARD.pack(pq, strides[0], pk, strides[1], pv, strides[2], po, so, decay, p, p, 0, packed)
+    _call(_lib_handle.im2win_seq_linear_step, "im2win_seq_linear_step", args, q, dev, None, None)
     return out
 
 
@@ -345,21 +408,20 @@ def linear_attention_backward(dout, q, k, v, log_decay, *, state=None, dstate=No
     returned; dstate_in, the gradient of ``state``, is None without one.
     log_decay is a constant of the model and gets no gradient. What lies past a
     sequence's end gets zeros."""
-    code, H, Dk, Dv, scale, decay = _linear_sizes(q, k, v, log_decay, scale, 4)
-    B, L = q.shape[:2]
-    qk, vo, st = (B, L, H, Dk), (B, L, H, Dv), (B, H, Dk, Dv)
-    tq, tk, tv = _tensor(q, "q", q, qk), _tensor(k, "k", q, qk), _tensor(v, "v", q, vo)
-    tdout = _tensor(dout, "dout", q, vo)
-    dq, a = _output(dq, "dq", q, qk)
-    dk, b = _output(dk, "dk", q, qk)
-    dv, c = _output(dv, "dv", q, vo)
-    dstate_in = None
-    if state is not None:
-        dstate_in = _torch.empty(st, dtype=_torch.float32, device=q.device)
-    args = _LINEAR.pack(*tq, *tk, *tv, *_NONE, decay, _floats(state, "state", q, st), 0, _ints(lens, "lens", q, (B,)),
-                        code, B, L, H, Dk, Dv, scale, *tdout, *a, *b, *c, _floats(dstate, "dstate", q, st),
-                        _floats(dstate_in, "dstate_in", q, st))
-    _call("im2win_seq_linear_backward", args, q, ws, _linear_bytes(B, L, H, Dk, Dv, True))
+    dev, plan, decay, pq, pk, pv = _linear_inputs(q, k, v, log_decay, scale, 4)
+    strides, vo, st, packed, sizes = plan
+    sdo = _strides("dout", dout.shape, dout.stride(), vo)
+    pdo = _pointer(dout, "dout", q.dtype, dev)
+    before, after = _floats(state, "state", dev, st), _floats(dstate, "dstate", dev, st)
+    dq, pdq, sdq = _output(dq, "dq", q, dev)
+    dk, pdk, sdk = _output(dk, "dk", k, dev)
+    dv, pdv, sdv = _output(dv, "dv", v, dev)
+    dstate_in = None if state is None else _torch.empty_like(state)
+    args = _LINEAR_BACKWARD.pack(pq, strides[0], pk, strides[1], pv, strides[2], decay, before, 0,
+                                 _ints(lens, "lens", dev, st[:1]), packed, pdo, sdo, pdq, sdq, pdk, sdk, pdv, sdv, after,
+                                 _floats(dstate_in, "dstate_in", dev, st))
+    _call(_lib_handle.im2win_seq_linear_backward, "im2win_seq_linear_backward", args, q, dev, ws,
+          _linear_bytes(*sizes, True))
     return dq, dk, dv, dstate_in
 
 
