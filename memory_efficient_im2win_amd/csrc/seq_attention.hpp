@@ -83,78 +83,92 @@ struct KeyStage {
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     }
 
-    // Looks up tile t's pages, a tile ahead of their use.
+    // Looks up tile t's pages, a tile ahead of their use. Where the rows of a
+    // copy lie in one page, lane j looks up the j-th copy's (id[0]); else every
+    // lane that of its row of each copy.
+    __device__ __forceinline__ bool even() const { return a.by_page.d % RPI == 0; }
+    __device__ __forceinline__ int lane_row() const { return ((lane & (N - 1)) * NW + wave) * RPI; }
     __device__ __forceinline__ void look_up(int t, Pages& p) const
     {
         if (!PAGED) return;
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-            p.id[j] = a.table[b * a.table_stride + a.by_page.div(min(t * kKeyTile + (int)row(j), kt.hi))];
-    }
-
-    // Tiles t of k and of v. The pages that were looked up are waited for once,
-    // before copies are under way that a wait for one of them would also wait for.
-    __device__ __forceinline__ void copy_both(int t, const Pages& p, u32 lds) const
-    {
-        if (PAGED) settle_loads();
-        copy(a.k, t, p, lds);
-        copy(a.v, t, p, lds + TILE);
-    }
-
-    // Tile t of x (k or v).
-    __device__ __forceinline__ void copy(const Tensor& x, int t, const Pages& p, u32 lds) const
-    {
-        const int k0 = t * kKeyTile;
-        const unsigned char* const zero = (const unsigned char*)kAbsent.zero;
-        if constexpr (!PAGED) {
-            const unsigned char* from = x.p + b * x.sb + hk * x.sh + (k0 + wave * RPI) * x.sl;
-            const u32 row_at = (lane / CH) * (u32)x.sl;
-            if (k0 + kKeyTile - 1 <= kt.hi && (k0 >= kt.lo || k0 + kKeyTile <= a.sinks)) {
-#pragma unroll
-                for (int j = 0; j < N; ++j)
-                    if ((int)chunk(j) * 8 < a.D)
-                        dma16(from + j * NW * RPI * x.sl, row_at + chunk(j) * 16, lds + (j * NW + wave) * 1024);
-            } else {
-#pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    const int key = k0 + (int)row(j);
-                    const bool there = key <= kt.hi && (key >= kt.lo || key < a.sinks);
-                    if ((int)chunk(j) * 8 < a.D)
-                        dma16(there ? from + j * NW * RPI * x.sl + row_at + chunk(j) * 16 : zero,
-                              lds + (j * NW + wave) * 1024);
-                }
-            }
+        const int32_t* const table = a.table + b * a.table_stride;
+        if (even()) {
+            p.id[0] = table[a.by_page.div(min(t * kKeyTile + lane_row(), kt.hi))];
             return;
         }
-        const unsigned char* from = x.p + hk * x.sh;
+#pragma unroll
+        for (int j = 0; j < N; ++j) p.id[j] = table[a.by_page.div(min(t * kKeyTile + (int)row(j), kt.hi))];
+    }
+
+    // Tiles t of k and of v.
+    __device__ __forceinline__ void copy_both(int t, const Pages& p, u32 lds) const
+    {
+        const int k0 = t * kKeyTile;
         const bool whole = k0 + kKeyTile - 1 <= kt.hi && (k0 >= kt.lo || k0 + kKeyTile <= a.sinks);
-        if (a.by_page.d % RPI == 0) {
-            // The rows of one copy lie in one page: its address is the same for the wave.
-            const u32 row_at = (lane / CH) * (u32)x.sl;
+        if constexpr (!PAGED) {
+            copy_rows(a.k, whole, k0, lds, [&](int j) { return a.k.p + b * a.k.sb + hk * a.k.sh + (k0 + (j * NW + wave) * RPI) * a.k.sl; });
+            copy_rows(a.v, whole, k0, lds + TILE, [&](int j) { return a.v.p + b * a.v.sb + hk * a.v.sh + (k0 + (j * NW + wave) * RPI) * a.v.sl; });
+            return;
+        }
+        // Waits for what was looked up, before copies are under way that a wait
+        // would also wait for.
+        settle_loads();
+        if (!even()) {
+            copy_odd(a.k, k0, p, lds);
+            copy_odd(a.v, k0, p, lds + TILE);
+            return;
+        }
+        // Every copy's offset at once, one a lane. (With a copy's address in
+        // scalar arithmetic, a tile of 16-token pages took 1 us more.)
+        const int id = p.id[0], key = k0 + lane_row(), at = key - (int)a.by_page.div(key) * (int)a.by_page.d;
+        const bool bad = (u32)id >= (u32)a.pages;
+        const int64_t to_k = id * a.k.sb + at * a.k.sl;
+        const int64_t to_v = a.k.sb == a.v.sb && a.k.sl == a.v.sl ? to_k : id * a.v.sb + at * a.v.sl;
+        const uint64_t bad_ones = __ballot(bad);
+        const auto from = [&](const Tensor& x, int64_t off, int j) {
+            const u32 lo = __builtin_amdgcn_readlane((int)off, j), hi = __builtin_amdgcn_readlane((int)(off >> 32), j);
+            return bad_ones >> j & 1 ? (const unsigned char*)nullptr : x.p + hk * x.sh + (int64_t)((uint64_t)hi << 32 | lo);
+        };
+        copy_rows(a.k, whole && !bad_ones, k0, lds, [&](int j) { return from(a.k, to_k, j); });
+        copy_rows(a.v, whole && !bad_ones, k0, lds + TILE, [&](int j) { return from(a.v, to_v, j); });
+    }
+
+private:
+    // The tile's rows of x, from(j) the address of the j-th copy's first row (null:
+    // a page outside the pool). plain: all rows are there.
+    template <typename F>
+    __device__ __forceinline__ void copy_rows(const Tensor& x, bool plain, int k0, u32 lds, F from) const
+    {
+        const u32 row_at = (lane / CH) * (u32)x.sl;
+        if (plain) {
 #pragma unroll
             for (int j = 0; j < N; ++j) {
-                const int id = uniform(p.id[j]), first = k0 + (j * NW + wave) * RPI;
-                const int at = first - (int)a.by_page.div(first) * (int)a.by_page.d;
-                const unsigned char* page = from + id * x.sb + at * x.sl;
-                const bool bad = (u32)id >= (u32)a.pages;
-                if ((int)chunk(j) * 8 >= a.D) continue;
-                if (whole && !bad) {
-                    dma16(page, row_at + chunk(j) * 16, lds + (j * NW + wave) * 1024);
-                } else {
-                    const int key = k0 + (int)row(j);
-                    const bool there = key <= kt.hi && (key >= kt.lo || key < a.sinks);
-                    const unsigned char* const e = bad ? (const unsigned char*)kAbsent.nan : page + row_at + chunk(j) * 16;
-                    dma16(there ? e : zero, lds + (j * NW + wave) * 1024);
-                }
+                const unsigned char* first = from(j);
+                if ((int)chunk(j) * 8 < a.D) dma16(first, row_at + chunk(j) * 16, lds + (j * NW + wave) * 1024);
             }
             return;
         }
 #pragma unroll
         for (int j = 0; j < N; ++j) {
+            const unsigned char* first = from(j);
+            const int key = k0 + (int)row(j);
+            const bool there = key <= kt.hi && (key >= kt.lo || key < a.sinks);
+            const unsigned char* e = first ? first + row_at + chunk(j) * 16 : (const unsigned char*)kAbsent.nan;
+            if (!there) e = (const unsigned char*)kAbsent.zero;
+            if ((int)chunk(j) * 8 < a.D) dma16(e, lds + (j * NW + wave) * 1024);
+        }
+    }
+
+    // The same where pages end inside a copy: every lane's own address.
+    __device__ __forceinline__ void copy_odd(const Tensor& x, int k0, const Pages& p, u32 lds) const
+    {
+        const unsigned char* const head = x.p + hk * x.sh;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
             const int key = k0 + (int)row(j), at = key - (int)a.by_page.div(key) * (int)a.by_page.d;
-            const unsigned char* e = from + p.id[j] * x.sb + at * x.sl + chunk(j) * 16;
-            if (p.id[j] < 0 || p.id[j] >= a.pages) e = (const unsigned char*)kAbsent.nan;
-            if (!(key <= kt.hi && (key >= kt.lo || key < a.sinks))) e = zero;
+            const unsigned char* e = head + p.id[j] * x.sb + at * x.sl + chunk(j) * 16;
+            if ((u32)p.id[j] >= (u32)a.pages) e = (const unsigned char*)kAbsent.nan;
+            if (!(key <= kt.hi && (key >= kt.lo || key < a.sinks))) e = (const unsigned char*)kAbsent.zero;
             if ((int)chunk(j) * 8 < a.D) dma16(e, lds + (j * NW + wave) * 1024);
         }
     }
