@@ -91,13 +91,15 @@ struct KeyStage {
     __device__ __forceinline__ void look_up(int t, Pages& p) const
     {
         if (!PAGED) return;
+        // The same loads either way: with a branch the compiler moved what they
+        // load, and waited for it and the copies before, at once (108 -> 117 us,
+        // a token each of 64 sequences of up to 8192 keys).
         const int32_t* const table = a.table + b * a.table_stride;
-        if (even()) {
-            p.id[0] = table[a.by_page.div(min(t * kKeyTile + lane_row(), kt.hi))];
-            return;
-        }
 #pragma unroll
-        for (int j = 0; j < N; ++j) p.id[j] = table[a.by_page.div(min(t * kKeyTile + (int)row(j), kt.hi))];
+        for (int j = 0; j < N; ++j) {
+            const int key = t * kKeyTile + (even() ? lane_row() : (int)row(j));
+            p.id[j] = table[a.by_page.div(min(key, kt.hi))];
+        }
     }
 
     // Tiles t of k and of v.
@@ -106,20 +108,34 @@ struct KeyStage {
         const int k0 = t * kKeyTile;
         const bool whole = k0 + kKeyTile - 1 <= kt.hi && (k0 >= kt.lo || k0 + kKeyTile <= a.sinks);
         if constexpr (!PAGED) {
-            copy_rows(a.k, whole, k0, lds, [&](int j) { return a.k.p + b * a.k.sb + hk * a.k.sh + (k0 + (j * NW + wave) * RPI) * a.k.sl; });
-            copy_rows(a.v, whole, k0, lds + TILE, [&](int j) { return a.v.p + b * a.v.sb + hk * a.v.sh + (k0 + (j * NW + wave) * RPI) * a.v.sl; });
+            copy_run(a.k, whole, a.k.p + b * a.k.sb + hk * a.k.sh + (k0 + wave * RPI) * a.k.sl, k0, lds);
+            copy_run(a.v, whole, a.v.p + b * a.v.sb + hk * a.v.sh + (k0 + wave * RPI) * a.v.sl, k0, lds + TILE);
             return;
         }
         // Waits for what was looked up, before copies are under way that a wait
         // would also wait for.
         settle_loads();
+        if (a.by_page.d % kKeyTile == 0) {  // the tile is in one page: as in a whole sequence
+            const int id = uniform(p.id[0]);
+            const bool bad = (u32)id >= (u32)a.pages;
+            const auto run = [&](const Tensor& x, u32 to) {
+                const unsigned char* const page = x.p + hk * x.sh + (uint32_t)id * (uint64_t)x.sb;
+                copy_rows(x, whole && !bad, k0, to, [&](int j) {
+                    const int row = k0 + (j * NW + wave) * RPI, at = row - (int)a.by_page.div(row) * (int)a.by_page.d;
+                    return bad ? (const unsigned char*)nullptr : page + at * x.sl;
+                });
+            };
+            run(a.k, lds);
+            run(a.v, lds + TILE);
+            return;
+        }
         if (!even()) {
             copy_odd(a.k, k0, p, lds);
             copy_odd(a.v, k0, p, lds + TILE);
             return;
         }
         // Every copy's offset at once, one a lane. (With a copy's address in
-        // scalar arithmetic, a tile of 16-token pages took 1 us more.)
+        // scalar arithmetic, a tile of 16-token pages took 0.5 us more.)
         const int id = p.id[0], key = k0 + lane_row(), at = key - (int)a.by_page.div(key) * (int)a.by_page.d;
         const bool bad = (u32)id >= (u32)a.pages;
         const int64_t to_k = id * a.k.sb + at * a.k.sl;
@@ -134,6 +150,17 @@ struct KeyStage {
     }
 
 private:
+    // The tile's rows of x, one after another in memory from `first` (this wave's).
+    __device__ __forceinline__ void copy_run(const Tensor& x, bool plain, const unsigned char* first, int k0, u32 lds) const
+    {
+        const int64_t step = NW * RPI * x.sl;
+        copy_rows(x, plain, k0, lds, [&](int) {
+            const unsigned char* const r = first;
+            first += step;
+            return r;
+        });
+    }
+
     // The tile's rows of x, from(j) the address of the j-th copy's first row (null:
     // a page outside the pool). plain: all rows are there.
     template <typename F>
