@@ -76,7 +76,6 @@ struct LinParams {
     const float* log_decay;
     const int32_t* lens;
     int jobs, B, L, H, nseg, seg_len;
-    bool fold;  // set by the launcher: no pass over the segments' states
 };
 // Segments of a call of `jobs` recurrences, and the workspace of one job.
 struct LinPlan {

@@ -12,7 +12,7 @@
 //
 // A long axis is cut into segments that run side by side: first each
 // segment's own state from zero, then the states before each segment (one
-// pass over them, or, for a few segments, at the start of the next kernel), then the outputs.
+// pass over them), then the outputs.
 //
 // A workgroup owns one segment of one head; a wave owns 32 columns (dv) of the
 // state, in fp32 registers for the whole walk, laid out as an operand:
@@ -26,11 +26,6 @@
 // bits, fp16 2, 22 bits, where the caller asks for the last state; two where the
 // state only leads to outputs (118 us against 116 with one); one for dk and dv
 // side by side, where two took 109 + 56 us and one takes 95 + 43.
-//
-// Measured on 32768 tokens, 16 heads of 128, bf16: segment states 62-65 us, the
-// states before them 16 us, outputs 117 us. All three are bound by memory: the
-// outputs move 0.57 GB (4.9 TB/s, 94% of a copy's rate). Backward, 2 x 8192 tokens,
-// 16 heads: dk and dv 43 + 95 us, dq 32 + 60 us.
 #include "seq_common.hpp"
 #include "seq_kernels.hpp"
 
@@ -175,32 +170,19 @@ __global__ __launch_bounds__(DVP * (PAIR ? 4 : 2), 2) void linear_kernel(const L
     floatx16_t S[MT] = {};
     float* seg_state = J.seg + (((int64_t)b * a.H + hd) * a.nseg + seg) * (DKP * DVP) + thread;
     const int64_t given = ((int64_t)b * a.H + hd) * J.dk * J.dv;
-    const auto given_state = [&](auto f) {  // f(mt, i, the register's element of a given state)
+    if (MODE == kOutputs) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) S[mt][i] = seg_state[(mt * 16 + i) * (NW * 64)];
+    } else if (MODE == kWhole && J.s_in) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const int dk = 32 * mt + 16 * (i / 8) + 8 * h + i % 8, dv = wave * 32 + col;
-                if (dk < J.dk && dv < J.dv) f(mt, i, given + (int64_t)dk * J.sk + (int64_t)dv * J.sv);
+                if (dk < J.dk && dv < J.dv) S[mt][i] = J.s_in[given + (int64_t)dk * J.sk + (int64_t)dv * J.sv];
             }
-    };
-    const auto add_own = [&](int j) {  // from the state before segment j to the one after
-        const float* own = seg_state + (int64_t)(j - seg) * (DKP * DVP);
-        const float fall = __builtin_amdgcn_exp2f(g * (float)min(max(n - j * a.seg_len, 0), a.seg_len));
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) S[mt][i] = fmaf(S[mt][i], fall, own[(mt * 16 + i) * (NW * 64)]);
-    };
-    if ((MODE == kWhole || (MODE == kOutputs && a.fold)) && J.s_in)
-        given_state([&](int mt, int i, int64_t at) { S[mt][i] = J.s_in[at]; });
-    if (MODE == kOutputs && a.fold) {
-        for (int j = 0; j < seg; ++j) add_own(j);
-    } else if (MODE == kOutputs) {
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) S[mt][i] = seg_state[(mt * 16 + i) * (NW * 64)];
     }
 
     // Decays inside a chunk: between tokens, from the chunk's start, to its end.
@@ -334,15 +316,13 @@ __global__ __launch_bounds__(DVP * (PAIR ? 4 : 2), 2) void linear_kernel(const L
 #pragma unroll
             for (int i = 0; i < 16; ++i) seg_state[(mt * 16 + i) * (NW * 64)] = S[mt][i];
     } else if (MODE == kWhole && J.s_out) {
-        given_state([&](int mt, int i, int64_t at) { J.s_out[at] = S[mt][i]; });
-    } else if (MODE == kOutputs && a.fold && J.s_out && seg == a.nseg - 1) {
-        // The last state from the segments' own ones, which hold more bits than
-        // the state that the outputs' walk ends with.
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) S[mt] = floatx16_t{};
-        if (J.s_in) given_state([&](int mt, int i, int64_t at) { S[mt][i] = J.s_in[at]; });
-        for (int j = 0; j < a.nseg; ++j) add_own(j);
-        given_state([&](int mt, int i, int64_t at) { J.s_out[at] = S[mt][i]; });
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int dk = 32 * mt + 16 * (i / 8) + 8 * h + i % 8, dv = wave * 32 + col;
+                if (dk < J.dk && dv < J.dv) J.s_out[given + (int64_t)dk * J.sk + (int64_t)dv * J.sv] = S[mt][i];
+            }
     }
 }
 
@@ -382,8 +362,7 @@ __global__ __launch_bounds__(256) void linear_join_kernel(const LinParams a)
 }
 
 // One token: out = scale q (a S + k v^T), the state updated in place, all in
-// fp32. Bound by the state's bytes, read and written once (64 sequences, 32 heads
-// of 128: 55 us, 4.9 TB/s; one sequence, 16 heads: 5 us, its launch). A workgroup owns
+// fp32. Bound by the state's bytes, read and written once. A workgroup owns
 // `cols` columns of one head's state; 4 columns a thread, rows side by side.
 template <bool BF>
 __global__ __launch_bounds__(256) void linear_step_kernel(const LinStep a, int cols, int blocks)
@@ -437,7 +416,7 @@ __global__ __launch_bounds__(256) void linear_step_kernel(const LinStep a, int c
 }
 
 template <bool BF, int DKP, int DVP, bool PAIR>
-int run(LinParams a, hipStream_t st)
+int run(const LinParams& a, hipStream_t st)
 {
     const unsigned heads = (unsigned)(a.B * a.H), all = heads * (unsigned)a.jobs;
     const unsigned grid = (PAIR ? heads : all) * (unsigned)a.nseg, threads = DVP * (PAIR ? 4 : 2);
@@ -446,17 +425,10 @@ int run(LinParams a, hipStream_t st)
         return launch_status();
     }
     bool wanted = false;
-    // Up to 4 segments: their workgroups add up the states before them by
-    // themselves, which saves a launch. (Not where the last state
-    // replaces the first one, which other workgroups may still have to read.)
-    a.fold = a.nseg <= 4;
-    for (int j = 0; j < a.jobs; ++j) {
-        wanted |= a.job[j].s_out != nullptr;
-        a.fold &= !a.job[j].s_out || a.job[j].s_out != a.job[j].s_in;
-    }
+    for (int j = 0; j < a.jobs; ++j) wanted |= a.job[j].s_out != nullptr;
     if (wanted) linear_kernel<BF, DKP, DVP, kStates, PAIR><<<grid, threads, 0, st>>>(a);
     else linear_kernel<BF, DKP, DVP, kRoughStates, PAIR><<<grid, threads, 0, st>>>(a);
-    if (!a.fold) linear_join_kernel<DKP, DVP><<<all * (DKP * DVP / 256), 256, 0, st>>>(a);
+    linear_join_kernel<DKP, DVP><<<all * (DKP * DVP / 256), 256, 0, st>>>(a);
     linear_kernel<BF, DKP, DVP, kOutputs, PAIR><<<grid, threads, 0, st>>>(a);
     return launch_status();
 }
