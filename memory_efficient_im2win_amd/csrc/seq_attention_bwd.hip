@@ -113,8 +113,8 @@ struct RowStage {
 // registers for a head of 128, which leaves room to read ahead from LDS; one
 // wave doing both had none, and took 405 us where this takes 205 (8192 tokens, 16
 // query and 4 key heads of 128, window 1024, bf16: 0.67 PFLOP/s). Bound by what a
-// step between two barriers waits for: matrix units busy 34% of the time, vector units
-// 34%, LDS 28%. Groups of 64 keys, two workgroups a CU, took 235 us.
+// step between two barriers waits for: matrix units busy 35% of the time, vector units
+// 36%, LDS 29%. Groups of 64 keys, two workgroups a CU, took 235 us.
 // Workgroups before the key tiles take the chunks of sink rows.
 template <bool BF, int DP, int NW>
 __global__ __launch_bounds__(NW * 64, 2) void attn_dkv_kernel(const AttnParams a)
@@ -310,7 +310,7 @@ __global__ __launch_bounds__(256) void attn_sink_join_kernel(const AttnParams a)
 // dQ of 128 flattened rows, 32 a wave, and their statistics: lse in log2 units
 // (+infinity where a row sees nothing or is padding, so that its P is 0) and D.
 // At the sizes above 128 us, 0.8 PFLOP/s; matrix units busy 43% of the time, vector
-// units 38%. A statistics kernel of its own took 14 us.
+// units 39%. A statistics kernel of its own took 14 us.
 template <bool BF, int DP>
 __global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnParams a)
 {

@@ -23,11 +23,11 @@
 //
 // Measured in bf16. 16384 tokens, 32 query and 8 key heads of 128, window 2048:
 // 565 us, 0.96 PFLOP/s, three quarters of a large library product's rate on the
-// same card. The matrix units are busy 48% of the time and the vector units 43%;
+// same card. The matrix units are busy 48% of the time and the vector units 50%;
 // without the copies the kernel would take a quarter less. Forming the next
 // tile's scores under this one's exponentials took 3% more, 256 rows a workgroup
-// 6%; wave priorities changed nothing. One token over 8192 keys, window 4096: 11 us
-// and 5 us for the join, bound by launches and first accesses. 64 sequences of up to
+// 6%; wave priorities changed nothing. One token over 8192 keys, window 4096: 10 us
+// and 4 us for the join, bound by launches and first accesses. 64 sequences of up to
 // 8192 keys over pages, window 2048: bound by the bytes of the keys, 5 TB/s.
 // 200 tokens, 8 query and 2 key heads of 64 in fp16: 7 us; one wave for a 32-row
 // tile took 13.

@@ -26,6 +26,11 @@
 // bits, fp16 2, 22 bits, where the caller asks for the last state; two where the
 // state only leads to outputs (118 us against 116 with one); one for dk and dv
 // side by side, where two took 109 + 56 us and one takes 95 + 43.
+//
+// Measured on 32768 tokens, 16 heads of 128, bf16: segment states 62-65 us, the
+// states before them 16 us, outputs 117 us. All three are bound by memory: the
+// outputs move 0.57 GB (4.9 TB/s, 94% of a copy's rate). Backward, 2 x 8192 tokens,
+// 16 heads: dk and dv 43 + 95 us, dq 32 + 60 us.
 #include "seq_common.hpp"
 #include "seq_kernels.hpp"
 
@@ -362,7 +367,8 @@ __global__ __launch_bounds__(256) void linear_join_kernel(const LinParams a)
 }
 
 // One token: out = scale q (a S + k v^T), the state updated in place, all in
-// fp32. Bound by the state's bytes, read and written once. A workgroup owns
+// fp32. Bound by the state's bytes, read and written once (64 sequences, 32 heads
+// of 128: 55 us, 4.9 TB/s; one sequence, 16 heads: 5 us, its launch). A workgroup owns
 // `cols` columns of one head's state; 4 columns a thread, rows side by side.
 template <bool BF>
 __global__ __launch_bounds__(256) void linear_step_kernel(const LinStep a, int cols, int blocks)

@@ -18,8 +18,8 @@ from test_gpu_sequence import TYPES, _bound, _check_forward, _ints, _linear_inpu
 pytestmark = pytest.mark.gpu
 
 
-# Sequences of a few segments, whose states are added up where they are needed,
-# or, where the last state replaces the first one, in a pass of their own.
+# Sequences of a few segments, with the last state apart from the first one and
+# in its place.
 @pytest.mark.parametrize("dtype", TYPES, ids=str)
 @pytest.mark.parametrize("state_given", ["none", "apart", "replaced"])
 @pytest.mark.parametrize("c", [
